@@ -52,6 +52,16 @@ class LvaHostStepBuffers(ctypes.Structure):
                 ("nnz", ctypes.c_void_p), ("events", ctypes.POINTER(ctypes.c_void_p)), ("num_events", ctypes.c_int)]
 
 
+class LvaPackedParams(ctypes.Structure):
+    """Mirror of ``lva_packed_params``."""
+    _fields_ = [("num_seqs", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("d", ctypes.c_int),
+                ("causal", ctypes.c_int), ("scale", ctypes.c_float), ("total_q", ctypes.c_int64),
+                ("total_k", ctypes.c_int64), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("o_token_stride", ctypes.c_int64), ("o_head_stride", ctypes.c_int64)]
+
+
 SIGNATURES = {
     "lva_status_string": (ctypes.c_char_p, [_c_int]),
     "lva_last_error_message": (ctypes.c_char_p, []),
@@ -81,6 +91,7 @@ SIGNATURES = {
     "lva_layer_step_host": (_c_int, [_vp, _vp, _vp, ctypes.POINTER(LvaLayerShape), ctypes.POINTER(LvaMaskParams),
                                      _vp, _c_int, _vp, _c_int, ctypes.POINTER(LvaHostStepBuffers), _c_int, _vp, _vp,
                                      _vp, ctypes.POINTER(ctypes.c_void_p)]),
+    "lva_packed_attn": (_c_int, [ctypes.POINTER(LvaPackedParams), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "lva_device_error": (_c_int, [_vp, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
     "lva_selftest_wait": (_c_int, [_c_int, _vp]),
 }
@@ -431,6 +442,42 @@ def lva_layer_step_host(qkv_host, o_host, lse_host, shape: LvaLayerShape, params
                                    ctypes.c_void_p(h2d.cuda_stream), ctypes.c_void_p(d2h.cuda_stream),
                                    ctypes.byref(done)))
     return done.value
+
+
+def _heads_view(t, name: str, shape):
+    """Checks a bf16 CUDA tensor [tokens, heads, d] on the current device whose rows are
+    contiguous (token and head strides are free: slices of a fused projection serve as they
+    are); returns (token stride, head stride)."""
+    import torch
+    _need(t is not None and t.is_cuda, f"{name} must be a CUDA tensor")
+    _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
+    current = torch.cuda.current_device()
+    _need(t.device.index == current, f"{name} is on cuda:{t.device.index}, the current device is cuda:{current}")
+    _need(tuple(t.shape) == shape, f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    st, sh, se = t.stride()
+    _need(se == 1, f"{name} must be contiguous in its last dimension")
+    # the stride of a dimension of one element is never walked, whatever the view says
+    return (st if shape[0] > 1 else shape[1] * max(sh, shape[2]) if shape[1] > 1 else shape[2]), sh
+
+
+def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = True):
+    """O, LSE of attention over packed sequences: q, o [total_q, Hq, d], k, v [total_k, Hkv, d]
+    (bf16, rows contiguous, token and head strides free), lse [Hq, total_q] (fp32), cu_q and
+    cu_k [sequences + 1] (int32, device).  Causal: a sequence's last query sees all its keys."""
+    import torch
+    _need(q.dim() == 3 and k.dim() == 3, "q and k must be [tokens, heads, d]")
+    tq, hq, d = q.shape
+    tk, hk = k.shape[:2]
+    qs, ks = _heads_view(q, "q", (tq, hq, d)), _heads_view(k, "k", (tk, hk, d))
+    vs, os = _heads_view(v, "v", (tk, hk, d)), _heads_view(o, "o", (tq, hq, d))
+    _cuda_tensor(lse, "lse", torch.float32, hq * tq)
+    _cuda_tensor(cu_q, "cu_q", torch.int32, 1)
+    _cuda_tensor(cu_k, "cu_k", torch.int32, cu_q.numel())
+    _need(cu_q.numel() == cu_k.numel(), "cu_q and cu_k must have the same number of entries")
+    p = LvaPackedParams(cu_q.numel() - 1, hq, hk, d, int(bool(causal)), scale, tq, tk, *qs, *ks, *vs, *os)
+    _check(lib.lva_packed_attn(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_q),
+                               _ptr(cu_k), ctypes.c_void_p(_stream(q.device))))
+    return o, lse
 
 
 def lva_device_error(stream=None):

@@ -1,5 +1,6 @@
 // api.cu -- the C ABI declared in include/lva.h: argument checks, status codes, the
 // per-thread error message, the per-device kernel error word, and dispatch to launchers.
+#include <cmath>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -418,6 +419,61 @@ lva_status lva_aggregate_masks(const uint8_t* masks, uint8_t* out, int prompts, 
   if (!masks || !out) return fail(LVA_ERR_INVALID_ARG, "aggregate: null pointer");
   AggregateArgs a{masks, out, prompts, count, rho * double(prompts)};
   return from_cuda(launch_aggregate(a, stream), "aggregate launch");
+}
+
+// A bf16 [tokens, heads, d] view: strides in elements, rows on 16-byte boundaries.  The TMA
+// takes strides below 2^40 bytes.
+static bool view_ok(int64_t token_stride, int64_t head_stride, int heads, int d) {
+  const int64_t most = int64_t(1) << 38;
+  if (token_stride < d || token_stride % 8 != 0 || token_stride > most) return false;
+  return heads == 1 || (head_stride >= d && head_stride % 8 == 0 && head_stride <= most);
+}
+
+// Checks of head counts, head dim and scale that the context calls share.
+static lva_status check_heads(const char* fn, int q_heads, int kv_heads, int d, float scale) {
+  if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0)
+    return fail(LVA_ERR_INVALID_ARG, "%s: kv_heads must divide q_heads, both >= 1", fn);
+  if (d != 64 && d != 128) return fail(LVA_ERR_UNSUPPORTED, "%s: head dim must be 64 or 128", fn);
+  if (!(scale > 0.f) || !std::isfinite(scale) || !std::isfinite(scale * 1.4426950408889634f))
+    return fail(LVA_ERR_INVALID_ARG, "%s: scale must be positive and finite", fn);
+  return LVA_OK;
+}
+
+lva_status lva_packed_attn(const lva_packed_params* p, const void* q, const void* k, const void* v, void* o,
+                           float* lse, const int32_t* cu_q, const int32_t* cu_k, cudaStream_t stream) {
+  if (p == nullptr) return fail(LVA_ERR_INVALID_ARG, "packed: null params");
+  const lva_status s = check_heads("packed", p->q_heads, p->kv_heads, p->d, p->scale);
+  if (s != LVA_OK) return s;
+  const int group = p->q_heads / p->kv_heads;
+  if (group > 128) return fail(LVA_ERR_UNSUPPORTED, "packed: at most 128 query heads per key/value head");
+  if (p->num_seqs < 0 || p->total_q < 0 || p->total_k < 0)
+    return fail(LVA_ERR_INVALID_ARG, "packed: num_seqs and totals must be >= 0");
+  if (p->total_q >= (int64_t(1) << 31) || p->total_k >= (int64_t(1) << 31))
+    return fail(LVA_ERR_UNSUPPORTED, "packed: totals must be < 2^31 tokens");
+  if (!view_ok(p->q_token_stride, p->q_head_stride, p->q_heads, p->d) ||
+      !view_ok(p->k_token_stride, p->k_head_stride, p->kv_heads, p->d) ||
+      !view_ok(p->v_token_stride, p->v_head_stride, p->kv_heads, p->d) ||
+      !view_ok(p->o_token_stride, p->o_head_stride, p->q_heads, p->d))
+    return fail(LVA_ERR_INVALID_ARG, "packed: strides must be multiples of 8 elements, at least d");
+  if ((p->total_q / (128 / group) + p->num_seqs) * p->kv_heads > int64_t(0x7fffffff))
+    return fail(LVA_ERR_UNSUPPORTED, "packed: too many tiles for one launch");
+  if (p->num_seqs == 0 || p->total_q == 0) return ok();
+  if (!q || !o || !lse || !cu_q || !cu_k || (p->total_k > 0 && (!k || !v)))
+    return fail(LVA_ERR_INVALID_ARG, "packed: null pointer");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16))
+    return fail(LVA_ERR_INVALID_ARG, "packed: q, k, v, o must be 16-byte aligned");
+  if (!aligned(lse, 4) || !aligned(cu_q, 4) || !aligned(cu_k, 4))
+    return fail(LVA_ERR_INVALID_ARG, "packed: lse, cu_q, cu_k must be 4-byte aligned");
+  int* err = device_error_word();
+  if (err == nullptr) return fail(LVA_ERR_CUDA, "packed: cannot locate the device error word");
+  PackedArgs a{q, k, v, o, lse, p->num_seqs, p->q_heads, p->kv_heads, p->d, p->total_q, p->total_k,
+               p->q_token_stride, p->q_head_stride, p->k_token_stride, p->k_head_stride,
+               p->v_token_stride, p->v_head_stride, p->o_token_stride, p->o_head_stride,
+               cu_q, cu_k, p->causal != 0, p->scale, 0, nullptr, nullptr, err};
+  const char* why = "launch";
+  const cudaError_t e = launch_packed(a, stream, &why);
+  if (e != cudaSuccess) return fail(LVA_ERR_CUDA, "packed: %s: %s", why, cudaGetErrorString(e));
+  return ok();
 }
 
 lva_status lva_selftest_wait(int mode, cudaStream_t stream) {

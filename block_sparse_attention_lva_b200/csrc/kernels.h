@@ -171,6 +171,95 @@ bool make_rows_map(CUtensorMap* m, const void* base, int64_t rows, int d, int bo
 bool make_window_gather_map(CUtensorMap* m, const void* base, int64_t planes, int windows, int window,
                             int d, int box_rows);
 
+// 3D tensor map over bf16 [tokens, heads, d] with the given token and head strides (elements),
+// box of 64 elements x box_heads x box_tokens, 128-byte swizzle: box rows are token-major,
+// the heads of a token next to one another.
+bool make_heads_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int d, int64_t token_stride,
+                    int64_t head_stride, int box_heads, int box_tokens);
+
+// Packed-sequence attention, or (splits > 0) all query tokens against a shared key prefix
+// with the parts left in part_o / part_lse (packed.cu).
+struct PackedArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  float* lse;
+  int num_seqs, q_heads, kv_heads, d;
+  int64_t total_q, total_k;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int causal;
+  float scale;
+  int splits;
+  float* part_o;
+  float* part_lse;
+  int* err;
+};
+cudaError_t launch_packed(const PackedArgs& a, cudaStream_t stream, const char** why);
+
+// A batch's own caches, a few query tokens per sequence, and the join with the prefix parts
+// (cache_attn.cu).
+struct CacheAttnArgs {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* lens;
+  void* o;
+  float* lse;
+  float* weight;             // NULL or [B, kv_heads, capacity], added to
+  int B, steps, q_heads, kv_heads, d;
+  int64_t prefix_len, capacity;
+  int64_t q_token, q_head, o_token, o_head;
+  float scale;
+  int splits;                // prefix parts
+  const float* part_o;       // [splits, kv_heads, B * steps, group, d]
+  const float* part_lse;
+  float* own_o;              // [slots, group * steps, d]
+  float* own_lse;            // [slots, group * steps], log2 units
+  float* scores;             // NULL or [B, kv_heads, group * steps, score_stride]
+  int64_t score_stride;
+  int* err;
+};
+// Most rows (query heads per key/value head x tokens per step) of one sequence.
+constexpr int kCacheMaxRows = 64;
+// Segments that the cache pass writes at most: one per (sequence, head) and one per worker.
+constexpr int kCacheWorkers = 296;
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream, const char** why);
+cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream);
+
+struct AppendArgs {
+  const void* k_new;
+  const void* v_new;
+  void* k_cache;
+  void* v_cache;
+  float* weight;             // NULL or [B, kv_heads, capacity]
+  const int32_t* lens;
+  int32_t* lens_out;
+  int B, steps, kv_heads, d;
+  int64_t capacity;
+  int64_t k_token, k_head, v_token, v_head;
+  int* err;
+};
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
+
+struct EvictArgs {
+  const void* k_cache;
+  const void* v_cache;
+  const float* weight;
+  const int32_t* lens;
+  void* k_out;
+  void* v_out;
+  float* weight_out;
+  int32_t* lens_out;
+  int32_t* kept;             // [B, kv_heads, budget]
+  int B, kv_heads, d;
+  int64_t capacity, budget, sinks, recent;
+  int* err;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+
 // Device error word of the current device (from api.cu).
 int* device_error_word();
 

@@ -1,0 +1,670 @@
+// packed.cu -- attention over packed sequences of different lengths, and over a key prefix
+// that a whole batch shares, for sm_100a (TMA + tcgen05 + TMEM).
+//
+// One work item is a tile of up to 128 rows of one key/value head: 128 / G consecutive query
+// tokens times the G query heads that share that key/value head (row r: token r / G, head
+// r % G), so grouped heads load each key tile once and short sequences fill a tile with
+// their heads.  Row i of a sequence with Lq queries and Lk keys sees the keys c < limit(i),
+//
+//   limit(i) = Lk, or with the causal mask min(Lk, i + Lk - Lq + 1) (<= 0: no key),
+//
+// and the kernel computes, over the 128-key blocks that any row of the tile sees,
+//
+//   O_i = sum_c 2^(x_ic - m_i) v_c / l_i,  l_i = sum_c 2^(x_ic - m_i),
+//   LSE_i = ln 2 (m_i + log2 l_i),         x_ic = scale log2(e) <q_i, k_c>,
+//
+// in one pass with a running reference m_i.  Blocks that every row of the tile sees in full
+// take a step without mask code; the others (the diagonal of a causal mask, the end of a
+// sequence) take the masked step, where an unseen key's weight is exactly zero.  V rows past
+// a sequence's end are zeroed in shared memory before they are multiplied, so whatever
+// memory holds there (another sequence, NaN) adds nothing.
+//
+// Shared prefix (p.splits > 0): one "sequence" of all query tokens of the batch against the
+// prefix keys, cut along the keys into p.splits parts so that few rows still fill the GPU;
+// each part stores its normalised O and its LSE (log2 units) in float32, joined later with
+// the parts of the sequences' own caches.
+//
+// Pipeline and warp roles are those of the block-sparse kernel (attn.cu): three S buffers in
+// TMEM next to O, P over its own S, Q K^T and P V issued by two threads, K and V rings of
+// three 128-row TMA tiles, eight softmax warps with half a row per thread, exponentials
+// against the current reference while the block's maximum is found alongside, O rescaled
+// only when a row's maximum grows by more than 2^8.
+#include <cstdint>
+#include <type_traits>
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace lva {
+namespace {
+
+constexpr int BM = 128, BN = 128;
+constexpr int kSoftmaxWarp0 = 2;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kVWarp = kSoftmaxWarp0 + kSoftmaxWarps;
+constexpr int kPVWarp = kVWarp + 1;
+constexpr int kThreads = 32 * (kPVWarp + 1);
+constexpr float kRescaleThreshold = 8.0f;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// One pair of exponentials in four on the FMA pipe (as in the block-sparse kernel).
+__device__ __forceinline__ constexpr bool poly_pair(int e) { return e % 4 == 3; }
+
+struct PackedParams {
+  int num_seqs;
+  int kv_heads, group, tok;        // tok = 128 / group query tokens per tile
+  int64_t total_q, total_k;
+  int64_t o_token, o_head;         // O strides in elements
+  const int32_t* cu_q;             // [num_seqs + 1]; unused for the shared prefix
+  const int32_t* cu_k;
+  int causal;
+  float scale_log2;                // scale * log2(e)
+  __nv_bfloat16* o;
+  float* lse;                      // [Hq, total_q]
+  int o_align32;
+  int splits;                      // 0: packed; > 0: parts of the shared prefix
+  float* part_o;                   // [splits, kv_heads, total_q, group, D]
+  float* part_lse;                 // [splits, kv_heads, total_q, group], log2 units
+  int* err;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int KST = 3, VST = 3, NSB = 3;
+  static constexpr int Q_BYTES = BM * D * 2;
+  static constexpr int KV_BYTES = BN * D * 2;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + Q_BYTES;
+  static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
+  static constexpr int OFF_BAR = OFF_V + VST * KV_BYTES;
+  // q_full, k_full/k_empty, v_full/v_empty, s_full, p_full, o_done, the two final drains and
+  // v_tail (the TMA of a V tile whose last rows are zeroed before v_full)
+  static constexpr int B_Q = 0, B_KF = 1, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST,
+                       B_SF = B_VE + VST, B_P = B_SF + NSB, B_O = B_P + NSB, B_FIN = B_O + NSB,
+                       B_FIN_PV = B_FIN + 1, B_VT = B_FIN_PV + 1, NUM_BARS = B_VT + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int SMEM_RAW = OFF_MISC + 16;
+  // at least 120 KB: one CTA, and one 512-column TMEM allocation, per SM
+  static constexpr int SMEM_BYTES = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  static constexpr uint32_t TM_S = 0, TM_O = 384;
+  static constexpr uint32_t IDESC_QK = idesc_bf16_f32(BM, BN, 0, 0);
+  static constexpr uint32_t IDESC_PV = idesc_bf16_f32(BM, D, 0, 1);
+};
+
+// A work item: rows [tok0, tok0 + rows / group) of the query tokens, key blocks [j0, j1) of
+// the key rows that start at k_row.
+struct Item {
+  int kvh;
+  int split;
+  int64_t tok0, q_end;     // first query token of the tile, end of its sequence
+  int64_t k_row, lk;       // first key row of the sequence, its keys
+  int64_t lim0;            // limit of the tile's first token before clamping to [0, lk]
+  int causal;
+  int j0, j_full, j1;      // blocks [j0, j_full) are seen in full by every row of the tile
+  bool live;               // false: nothing to do
+};
+
+// Largest s with start(s) <= slot, start(s) = cu[s] / tok + s, found by the whole warp, 32
+// probes a round; -1 when there is none.  start is strictly increasing for a valid cu, and
+// sequence s needs at most start(s + 1) - start(s) tiles; whatever cu holds, the answer stays
+// in [-1, n).
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int n, int tok, int64_t slot) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, cnt = n;
+  for (;;) {
+    const int step = (cnt + 31) / 32;
+    const int idx = lo + lane * step;
+    bool le = false;
+    if (lane * step < cnt) le = int64_t(__ldg(cu + idx) / tok) + idx <= slot;
+    const int k = __popc(__ballot_sync(0xffffffffu, le));
+    if (k == 0) return lo == 0 ? -1 : lo;
+    const int end = lo + cnt;
+    lo += (k - 1) * step;
+    if (step == 1) return lo;
+    cnt = step < end - lo ? step : end - lo;
+  }
+}
+
+__device__ __forceinline__ Item item_at(const PackedParams& p, int64_t bid) {
+  Item w;
+  w.live = false;
+  w.split = 0;
+  w.kvh = int(bid % p.kv_heads);
+  const int64_t rest = bid / p.kv_heads;
+  if (p.splits > 0) {
+    // Shared prefix: parts fastest after the head, so that the parts of a tile run together.
+    w.split = int(rest % p.splits);
+    w.tok0 = (rest / p.splits) * p.tok;
+    w.q_end = p.total_q;
+    w.k_row = 0;
+    w.lk = p.total_k;
+    w.lim0 = p.total_k;
+    w.causal = 0;
+    const int64_t nblk = (p.total_k + BN - 1) / BN;
+    w.j0 = int(nblk * w.split / p.splits);
+    w.j1 = int(nblk * (w.split + 1) / p.splits);
+    const int full = int(p.total_k / BN);
+    w.j_full = w.j1 < full ? w.j1 : full;
+    if (w.j_full < w.j0) w.j_full = w.j0;
+    w.live = w.tok0 < w.q_end;
+    return w;
+  }
+  // Packed: the last tiles of the last sequence first (a causal tile's work grows with its
+  // place, so the shortest tiles fill the tail), the heads of a tile next to one another.
+  const int64_t slots = p.total_q / p.tok + p.num_seqs;
+  const int64_t slot = slots - 1 - rest;
+  const int s = find_sequence(p.cu_q, p.num_seqs, p.tok, slot);
+  if (s < 0) return w;
+  const int64_t a = __ldg(p.cu_q + s), b = __ldg(p.cu_q + s + 1);
+  const int64_t ka = __ldg(p.cu_k + s), kb = __ldg(p.cu_k + s + 1);
+  if (!(a >= 0 && a <= b && b <= p.total_q && ka >= 0 && ka <= kb && kb <= p.total_k)) return w;
+  const int64_t tile = slot - (a / p.tok + s);
+  const int64_t i0 = tile * p.tok;                       // first token of the tile in its sequence
+  if (tile < 0 || i0 >= b - a) return w;
+  const int64_t lq = b - a, lk = kb - ka;
+  const int64_t last = (i0 + p.tok < lq ? i0 + p.tok : lq) - 1;
+  w.tok0 = a + i0;
+  w.q_end = b;
+  w.k_row = ka;
+  w.lk = lk;
+  w.causal = p.causal;
+  w.lim0 = p.causal ? i0 + lk - lq + 1 : lk;
+  int64_t lim_last = p.causal ? last + lk - lq + 1 : lk;
+  if (lim_last > lk) lim_last = lk;
+  if (lim_last < 0) lim_last = 0;
+  int64_t lim_first = w.lim0 > lk ? lk : w.lim0;
+  if (lim_first < 0) lim_first = 0;
+  w.j0 = 0;
+  w.j1 = int((lim_last + BN - 1) / BN);
+  w.j_full = int(lim_first / BN);
+  w.live = true;
+  return w;
+}
+
+// O *= alpha for this thread's half row, out of line (rare).
+template <int DH>
+__device__ __noinline__ void rescale_o(uint32_t taddr, float alpha) {
+#pragma unroll 1
+  for (int q = 0; q < DH / 32; ++q) {
+    uint32_t ov[32];
+    tmem_ld_16x2_32<DH>(taddr + q * 32, ov);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+    tmem_st_16x2_32<DH>(taddr + q * 32, ov);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
+    const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+    const __grid_constant__ CUtensorMap tm_v, const PackedParams p) {
+  using C = Cfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t s_base = smem_u32(smem);
+  if (s_base & 1023u) {                           // never expected; checked rather than assumed
+    if (threadIdx.x == 0) report_fault(p.err, 4, 1023);
+    return;
+  }
+  // The first CTA checks both length lists: a list that falls or leaves its buffer is
+  // reported, and the sequences it spoils are skipped where they are met.
+  if (blockIdx.x == 0 && p.splits == 0) {
+    for (int s = threadIdx.x; s < p.num_seqs; s += kThreads) {
+      const int64_t a = __ldg(p.cu_q + s), b = __ldg(p.cu_q + s + 1);
+      const int64_t ka = __ldg(p.cu_k + s), kb = __ldg(p.cu_k + s + 1);
+      if (!(a >= 0 && a <= b && b <= p.total_q && ka >= 0 && ka <= kb && kb <= p.total_k))
+        report_fault(p.err, 1, s);
+    }
+  }
+  const Item w = item_at(p, blockIdx.x);
+  if (!w.live) return;                            // the whole CTA: same item in every warp
+  const int n = w.j1 - w.j0;
+
+  const uint32_t sQ = s_base + C::OFF_Q, sK = s_base + C::OFF_K, sV = s_base + C::OFF_V;
+  const uint32_t bar0 = s_base + C::OFF_BAR;
+  const uint32_t bar_q = bar0 + 8u * C::B_Q;
+  auto bar_k_full = [&](int s) { return bar0 + 8u * (C::B_KF + s); };
+  auto bar_k_empty = [&](int s) { return bar0 + 8u * (C::B_KE + s); };
+  auto bar_v_full = [&](int s) { return bar0 + 8u * (C::B_VF + s); };
+  auto bar_v_empty = [&](int s) { return bar0 + 8u * (C::B_VE + s); };
+  auto bar_s_full = [&](int b) { return bar0 + 8u * (C::B_SF + b); };
+  auto bar_p_full = [&](int b) { return bar0 + 8u * (C::B_P + b); };
+  auto bar_o_done = [&](int b) { return bar0 + 8u * (C::B_O + b); };
+  const uint32_t bar_final = bar0 + 8u * C::B_FIN;
+  const uint32_t bar_final_pv = bar0 + 8u * C::B_FIN_PV;
+  const uint32_t bar_v_tail = bar0 + 8u * C::B_VT;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  volatile int* never = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // stays zero
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar_q, 1);
+    for (int s = 0; s < C::KST; ++s) { mbar_init(bar_k_full(s), 1); mbar_init(bar_k_empty(s), 1); }
+    for (int s = 0; s < C::VST; ++s) { mbar_init(bar_v_full(s), 1); mbar_init(bar_v_empty(s), 1); }
+    for (int b = 0; b < C::NSB; ++b) {
+      mbar_init(bar_s_full(b), 1);
+      mbar_init(bar_p_full(b), kSoftmaxWarps);
+      mbar_init(bar_o_done(b), 1);
+    }
+    mbar_init(bar_final, 1);
+    mbar_init(bar_final_pv, 1);
+    mbar_init(bar_v_tail, 1);
+    *abort_flag = 0;
+    *never = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) { tmem_alloc(smem_u32(tmem_slot), kTmemCols); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer: Q, K
+    if (lane == 0 && n > 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      mbar_arrive_expect_tx(bar_q, uint32_t(p.group * p.tok * D * 2));
+      for (int c = 0; c < D / 64; ++c)
+        tma_load_3d(sQ + c * BM * 128, &tm_q, c * 64, w.kvh * p.group, int32_t(w.tok0), bar_q);
+      int t = 0;
+      for (; t < n; ++t) {
+        const int s = t % C::KST;
+        if (t >= C::KST && !mbar_wait_sleep(bar_k_empty(s), ((t / C::KST) - 1) & 1, abort_flag)) {
+          *abort_flag = 1; report_fault(p.err, 5, 21); break;
+        }
+        mbar_arrive_expect_tx(bar_k_full(s), C::KV_BYTES);
+        for (int c = 0; c < D / 64; ++c)
+          tma_load_3d(sK + s * C::KV_BYTES + c * BN * 128, &tm_k, c * 64, w.kvh,
+                      int32_t(w.k_row + int64_t(w.j0 + t) * BN), bar_k_full(s));
+      }
+      if (*abort_flag) {
+        for (int u = t > C::KST ? t - C::KST : 0; u < t; ++u)
+          mbar_wait(bar_k_full(u % C::KST), (u / C::KST) & 1, never);
+        mbar_wait(bar_q, 0, never);
+      }
+    }
+  } else if (warp == kVWarp) {
+    // ------------------------------------------------------------ TMA producer: V
+    if (n > 0) {
+      if (lane == 0) tma_prefetch_desc(&tm_v);
+      bool ok = true;
+      int t = 0;
+      for (; t < n; ++t) {
+        const int s = t % C::VST;
+        const int64_t left = w.lk - int64_t(w.j0 + t) * BN;      // keys of the sequence from here on
+        const bool tail = left < BN;                             // at most the last block
+        if (lane == 0) {
+          if (t >= C::VST && !mbar_wait_sleep(bar_v_empty(s), ((t / C::VST) - 1) & 1, abort_flag)) {
+            *abort_flag = 1; report_fault(p.err, 5, 22); ok = false;
+          } else {
+            const uint32_t bar = tail ? bar_v_tail : bar_v_full(s);
+            mbar_arrive_expect_tx(bar, C::KV_BYTES);
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(sV + s * C::KV_BYTES + c * BN * 128, &tm_v, c * 64, w.kvh,
+                          int32_t(w.k_row + int64_t(w.j0 + t) * BN), bar);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (tail) {
+          // Rows past the sequence's end hold other sequences' values, or anything: zeroed,
+          // because their weight of zero times NaN or infinity would not be zero.
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_v_tail, 0, never));
+          if (ok) {
+            for (int c = 0; c < D / 64; ++c) {
+              uint8_t* rows = smem + C::OFF_V + s * C::KV_BYTES + c * BN * 128;
+              for (int x = int(left) * 8 + lane; x < BN * 8; x += 32)
+                reinterpret_cast<uint4*>(rows)[x] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_v_full(s));
+          } else if (lane == 0) {
+            *abort_flag = 1; report_fault(p.err, 5, 23);
+          }
+        }
+      }
+      if (lane == 0 && *abort_flag) {
+        for (int u = t > C::VST ? t - C::VST : 0; u < t; ++u)
+          mbar_wait(bar_v_full(u % C::VST), (u / C::VST) & 1, never);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer: S = Q K^T
+    if (lane == 0 && n > 0) {
+      const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024);
+      const uint64_t k_desc = smem_desc_sw128(sK, 16, 1024);
+      bool ok = mbar_wait_sleep(bar_q, 0, abort_flag);
+      bool any_mma = false;
+      for (int t = 0; ok && t < n; ++t) {
+        const int s = t % C::KST, b = t % C::NSB;
+        if (!mbar_wait_sleep(bar_k_full(s), (t / C::KST) & 1, abort_flag)) { ok = false; break; }
+        if (t >= C::NSB && !mbar_wait_sleep(bar_o_done(b), ((t / C::NSB) - 1) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t ks = k_desc + uint64_t((s * C::KV_BYTES) >> 4);
+        const uint32_t s_tm = tmem + C::TM_S + 128 * b;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_f16_ss(s_tm, q_desc + uint64_t(((kk / 4) * BM * 128 + (kk % 4) * 32) >> 4),
+                      ks + uint64_t(((kk / 4) * BN * 128 + (kk % 4) * 32) >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
+        umma_commit(bar_s_full(b));
+        umma_commit(bar_k_empty(s));
+        any_mma = true;
+      }
+      if (!ok) { *abort_flag = 1; report_fault(p.err, 5, 24); }
+      if (any_mma) {
+        umma_commit(bar_final);
+        mbar_wait(bar_final, 0, never);
+      }
+    }
+  } else if (warp == kPVWarp) {
+    // ------------------------------------------------------------ MMA issuer: O += P V
+    if (lane == 0 && n > 0) {
+      const uint64_t v_desc = smem_desc_sw128(sV, BN * 128, 1024);
+      bool ok = true, any_mma = false;
+      for (int t = 0; ok && t < n; ++t) {
+        const int s = t % C::VST, b = t % C::NSB;
+        if (!mbar_wait_sleep(bar_p_full(b), (t / C::NSB) & 1, abort_flag)) { ok = false; break; }
+        if (!mbar_wait_sleep(bar_v_full(s), (t / C::VST) & 1, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t vs = v_desc + uint64_t((s * C::KV_BYTES) >> 4);
+        const uint32_t p_tm = tmem + C::TM_S + 128 * b;
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          umma_f16_ts(tmem + C::TM_O, p_tm + kk * 8, vs + uint64_t((kk * 16 * 128) >> 4), C::IDESC_PV,
+                      (t > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(bar_v_empty(s));
+        umma_commit(bar_o_done(b));
+        any_mma = true;
+      }
+      if (!ok) { *abort_flag = 1; report_fault(p.err, 5, 25); }
+      if (any_mma) {
+        umma_commit(bar_final_pv);
+        mbar_wait(bar_final_pv, 0, never);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax + epilogue
+    // Thread = (row, column half): lane t and t + 16 hold the halves of one row.
+    constexpr int HALF = BN / 2, DH = D / 2;
+    const int quarter = warp & 3, sel = (warp - kSoftmaxWarp0) >> 2;
+    const int hf = lane >> 4;
+    const int row = quarter * 32 + sel * 16 + (lane & 15);
+    const uint32_t lane_off = uint32_t(quarter * 32 + sel * 16) << 16;
+    const float c = p.scale_log2;
+    const int tok_in = row / p.group;
+    const int64_t token = w.tok0 + tok_in;
+    const bool store = row < p.tok * p.group && token < w.q_end;
+    // Keys this row sees, counted from the sequence's first key.
+    int64_t limit = w.causal ? w.lim0 + tok_in : w.lim0;
+    limit = limit > w.lk ? w.lk : limit;
+    const bool sees = store && limit > 0;
+    bool ok = true;
+    float m_ref = -INFINITY;                       // reference max in log2 units
+    float l = 0.f;                                 // this half's share of the row sum
+
+    // One key block t; false when a wait gives up.  Masked: an unseen key's weight is zero
+    // (the MUFU's 2^-inf; the polynomial would give 2^-125).
+    auto step = [&](int t, auto masked_tag) -> bool {
+      constexpr bool MASKED = decltype(masked_tag)::value;
+      const int b = t % C::NSB;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full(b), (t / C::NSB) & 1, abort_flag))) return false;
+      tc_fence_after();
+      uint32_t sr[HALF];
+#pragma unroll
+      for (int q = 0; q < HALF / 32; ++q)
+        tmem_ld_16x2_32<HALF>(tmem + lane_off + C::TM_S + 128 * b + q * 32,
+                              *reinterpret_cast<uint32_t(*)[32]>(sr + q * 32));
+      tmem_wait_ld();
+      if constexpr (MASKED) {
+        const int64_t left = limit - (int64_t(w.j0 + t) * BN + hf * HALF);
+        const int vis = left > HALF ? HALF : int(left < 0 ? 0 : left);
+#pragma unroll
+        for (int e = 0; e < HALF; ++e)
+          if (e >= vis) sr[e] = __float_as_uint(-INFINITY);
+      }
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < HALF / 2; ++e)
+        m4[e & 3] = fmax3(m4[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+      float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      const float m_old = m_ref;
+      if (mx > m_ref + kRescaleThreshold || m_ref == -INFINITY) m_ref = fmaxf(mx, m_ref);
+      const float alpha = (m_old == m_ref) ? 1.f : ex2_approx(m_old - m_ref);
+      const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+      __syncwarp();                                // every lane's S is loaded: P may go over it
+      const uint32_t p_tm = tmem + lane_off + C::TM_S + 128 * b;
+      uint32_t pk[HALF / 2];
+      const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_use, -m_use);
+      uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+      for (int e = 0; e < HALF / 2; ++e) {
+        const uint64_t x2 = f2_fma(f2_pack_bits(sr[2 * e], sr[2 * e + 1]), c2, nm2);
+        uint64_t p2;
+        if (!MASKED && poly_pair(e)) {
+          p2 = exp2_poly_f2(x2);
+        } else {
+          float x0, x1;
+          f2_unpack(x2, x0, x1);
+          p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
+        }
+        acc[e & 1] = f2_add(acc[e & 1], p2);
+        float p0, p1;
+        f2_unpack(p2, p0, p1);
+        pk[e] = pack_bf16x2(p0, p1);               // P in bf16: the MMA's operand type
+        if (e == 15) tmem_st_16x2_16<HALF / 2>(p_tm, *reinterpret_cast<const uint32_t(*)[16]>(pk));
+      }
+      tmem_st_16x2_16<HALF / 2>(p_tm + 16, *reinterpret_cast<const uint32_t(*)[16]>(pk + 16));
+      float a0, a1, b0, b1;
+      f2_unpack(acc[0], a0, a1);
+      f2_unpack(acc[1], b0, b1);
+      l = l * alpha + ((a0 + a1) + (b0 + b1));
+      if (t >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_o_done((t - 1) % C::NSB), ((t - 1) / C::NSB) & 1, abort_flag)))
+          return false;
+        tc_fence_after();
+        rescale_o<DH>(tmem + lane_off + C::TM_O, alpha);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_p_full(b));
+      return true;
+    };
+
+    // A block that every row sees, after the first: exponentials against the current
+    // reference while the block max is found alongside; given up (2) before anything is
+    // stored when a row's max outgrows its reference by 2^8.
+    auto step_spec = [&](int t) -> int {
+      const int b = t % C::NSB;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full(b), (t / C::NSB) & 1, abort_flag))) return 0;
+      tc_fence_after();
+      uint32_t sr[HALF];
+#pragma unroll
+      for (int q = 0; q < HALF / 32; ++q)
+        tmem_ld_16x2_32<HALF>(tmem + lane_off + C::TM_S + 128 * b + q * 32,
+                              *reinterpret_cast<uint32_t(*)[32]>(sr + q * 32));
+      tmem_wait_ld();
+      const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-m_ref, -m_ref);
+      uint64_t acc[2] = {0ull, 0ull};
+      float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      uint32_t pk[HALF / 2];
+#pragma unroll
+      for (int e = 0; e < HALF / 2; ++e) {
+        m4[e & 3] = fmax3(m4[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+        const uint64_t x2 = f2_fma(f2_pack_bits(sr[2 * e], sr[2 * e + 1]), c2, nm2);
+        uint64_t p2;
+        if (poly_pair(e)) {
+          p2 = exp2_poly_f2(x2);
+        } else {
+          float x0, x1;
+          f2_unpack(x2, x0, x1);
+          p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
+        }
+        acc[e & 1] = f2_add(acc[e & 1], p2);
+        float p0, p1;
+        f2_unpack(p2, p0, p1);
+        pk[e] = pack_bf16x2(p0, p1);
+      }
+      float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      if (__any_sync(0xffffffffu, sees && (mx > m_ref + kRescaleThreshold || m_ref == -INFINITY))) return 2;
+      tmem_st_16x2_32<HALF / 2>(tmem + lane_off + C::TM_S + 128 * b, *reinterpret_cast<const uint32_t(*)[32]>(pk));
+      tmem_wait_st();
+      float a0, a1, b0, b1;
+      f2_unpack(acc[0], a0, a1);
+      f2_unpack(acc[1], b0, b1);
+      l = l + ((a0 + a1) + (b0 + b1));
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_p_full(b));
+      return 1;
+    };
+
+    const int t_full = w.j_full - w.j0;
+    int t = 0;
+    if (!__any_sync(0xffffffffu, store)) {
+      // No row of this warp is stored (a tile of few rows): its P may hold anything.
+      for (; ok && t < n; ++t) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(t % C::NSB), (t / C::NSB) & 1, abort_flag));
+        if (ok && lane == 0) mbar_arrive(bar_p_full(t % C::NSB));
+      }
+    }
+    for (; ok && t < t_full; ++t) {
+      int r = 2;
+      if (t > 0) r = step_spec(t);
+      if (r == 0) ok = false;
+      else if (r == 2) ok = step(t, std::false_type{});
+    }
+    for (; ok && t < n; ++t) ok = step(t, std::true_type{});
+
+    // ---------------------------------------------------------- epilogue
+    if (ok && n > 0) {
+      const int u = n - 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_o_done(u % C::NSB), (u / C::NSB) & 1, abort_flag));
+      tc_fence_after();
+    }
+    if (ok) {
+      const float l_row = l + __shfl_xor_sync(0xffffffffu, l, 16);
+      const bool none = !sees || l_row == 0.f;     // a NaN sum goes through as NaN
+      const float inv_l = none ? 0.f : 1.f / l_row;
+      const int head = w.kvh * p.group + (row - tok_in * p.group);
+      const int64_t part_row = ((int64_t(w.split) * p.kv_heads + w.kvh) * p.total_q + token) * p.group +
+                               (row - tok_in * p.group);
+#pragma unroll 1
+      for (int q = 0; q < DH / 32; ++q) {
+        uint32_t ov[32] = {};
+        __syncwarp();                              // the load is the whole warp's
+        if (n > 0) {
+          tmem_ld_16x2_32<DH>(tmem + lane_off + C::TM_O + q * 32, ov);
+          tmem_wait_ld();
+        }
+        if (!store) {
+        } else if (p.splits > 0) {
+          float* dst = p.part_o + part_row * D + hf * DH + q * 32;
+#pragma unroll
+          for (int e4 = 0; e4 < 8; ++e4) {
+            float4 f;
+            f.x = none ? 0.f : __uint_as_float(ov[4 * e4]) * inv_l;
+            f.y = none ? 0.f : __uint_as_float(ov[4 * e4 + 1]) * inv_l;
+            f.z = none ? 0.f : __uint_as_float(ov[4 * e4 + 2]) * inv_l;
+            f.w = none ? 0.f : __uint_as_float(ov[4 * e4 + 3]) * inv_l;
+            reinterpret_cast<float4*>(dst)[e4] = f;
+          }
+        } else {
+          __nv_bfloat16* dst = p.o + token * p.o_token + int64_t(head) * p.o_head + hf * DH + q * 32;
+          uint32_t wv[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            wv[e] = none ? 0u : pack_bf16x2(__uint_as_float(ov[2 * e]) * inv_l, __uint_as_float(ov[2 * e + 1]) * inv_l);
+          if (p.o_align32) {
+            st_global_v8(dst, *reinterpret_cast<const uint32_t(*)[8]>(wv));
+            st_global_v8(dst + 16, *reinterpret_cast<const uint32_t(*)[8]>(wv + 8));
+          } else {
+#pragma unroll
+            for (int e4 = 0; e4 < 4; ++e4)
+              reinterpret_cast<uint4*>(dst)[e4] = make_uint4(wv[4 * e4], wv[4 * e4 + 1], wv[4 * e4 + 2], wv[4 * e4 + 3]);
+          }
+        }
+      }
+      if (store && hf == 0) {
+        const float lse2 = none ? -INFINITY : m_ref + __log2f(l_row);
+        if (p.splits > 0) p.part_lse[part_row] = lse2;
+        else p.lse[int64_t(head) * p.total_q + token] = lse2 * kLn2;
+      }
+    } else {
+      *abort_flag = 1;
+      if (lane == 0) report_fault(p.err, 5, 26);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why) {
+  using C = Cfg<D>;
+  const int group = a.q_heads / a.kv_heads, tok = BM / group;
+  CUtensorMap tq, tk, tv;
+  // Without keys nothing is loaded: the maps then describe Q's rows.
+  const bool keys = a.total_k > 0;
+  if (!make_heads_map(&tq, a.q, a.total_q, a.q_heads, D, a.q_token, a.q_head, group, tok) ||
+      !make_heads_map(&tk, keys ? a.k : a.q, keys ? a.total_k : a.total_q, keys ? a.kv_heads : a.q_heads, D,
+                      keys ? a.k_token : a.q_token, keys ? a.k_head : a.q_head, 1, BN) ||
+      !make_heads_map(&tv, keys ? a.v : a.q, keys ? a.total_k : a.total_q, keys ? a.kv_heads : a.q_heads, D,
+                      keys ? a.v_token : a.q_token, keys ? a.v_head : a.q_head, 1, BN)) {
+    *why = "cuTensorMapEncodeTiled failed or is unavailable";
+    return cudaErrorInvalidValue;
+  }
+  static DeviceFlags attr_set = {};
+  cudaError_t e = once_per_device(attr_set, [] {
+    return cudaFuncSetAttribute(packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  });
+  if (e != cudaSuccess) { *why = "cudaFuncSetAttribute(max dynamic smem) failed"; return e; }
+  PackedParams p;
+  p.num_seqs = a.num_seqs;
+  p.kv_heads = a.kv_heads;
+  p.group = group;
+  p.tok = tok;
+  p.total_q = a.total_q;
+  p.total_k = a.total_k;
+  p.o_token = a.o_token;
+  p.o_head = a.o_head;
+  p.cu_q = a.cu_q;
+  p.cu_k = a.cu_k;
+  p.causal = a.causal;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.o_align32 = ((reinterpret_cast<uintptr_t>(a.o) & 31) == 0 && a.o_token % 16 == 0 && a.o_head % 16 == 0) ? 1 : 0;
+  p.splits = a.splits;
+  p.part_o = a.part_o;
+  p.part_lse = a.part_lse;
+  p.err = a.err;
+  const int64_t tiles = a.splits > 0 ? (a.total_q + tok - 1) / tok * a.splits : a.total_q / tok + a.num_seqs;
+  packed_attn_kernel<D><<<dim3(unsigned(tiles * a.kv_heads)), kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_packed(const PackedArgs& a, cudaStream_t stream, const char** why) {
+  if (a.d == 128) return launch_d<128>(a, stream, why);
+  if (a.d == 64) return launch_d<64>(a, stream, why);
+  *why = "unsupported d";
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace lva

@@ -60,4 +60,19 @@ bool make_window_gather_map(CUtensorMap* m, const void* base, int64_t planes, in
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_heads_map(CUtensorMap* m, const void* base, int64_t tokens, int heads, int d, int64_t token_stride,
+                    int64_t head_stride, int box_heads, int box_tokens) {
+  EncodeTiledFn fn = encode_tiled();
+  if (fn == nullptr) return false;
+  // [tokens, heads, d] with any token and head stride, innermost first.  The stride of a
+  // single head is never walked; d stands in for whatever the caller's view says.
+  const cuuint64_t dims[3] = {cuuint64_t(d), cuuint64_t(heads), cuuint64_t(tokens)};
+  const cuuint64_t strides[2] = {cuuint64_t(heads > 1 ? head_stride : d) * 2, cuuint64_t(token_stride) * 2};
+  const cuuint32_t box[3] = {64u, cuuint32_t(box_heads), cuuint32_t(box_tokens)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace lva

@@ -468,6 +468,55 @@ lva_status lva_layer_step_host(const void* qkv_host, void* o_host, float* lse_ho
                                cudaEvent_t* done);
 
 /*
+ * lva_packed_attn -- softmax attention over packed sequences of different lengths.
+ *
+ * The text side of a video model and its step-by-step rollouts: prompts of a batch one after
+ * another in one buffer, causal or not, with query heads that share key/value heads.  The
+ * pages describe one sequence of one length per call and have no counterpart.
+ *
+ * Sequence s has the queries cu_q[s] .. cu_q[s+1]-1 and the keys cu_k[s] .. cu_k[s+1]-1 (Lq
+ * and Lk of them; either may be 0).  Query head h reads key/value head h / (q_heads/kv_heads).
+ * Query i of a sequence sees its key c when causal == 0 or c <= i + Lk - Lq (the last query
+ * sees every key: new tokens against what is there already), and
+ *   LSE[h][i] = ln sum_c exp(scale <q_i, k_c>),  O_i = sum_c exp(scale <q_i, k_c> - LSE) v_c.
+ * A query that sees no key gets O = 0 and LSE = -inf.
+ *
+ * q, o: device, bf16, element (token t, head h, e) at t * token_stride + h * head_stride + e;
+ * k, v the same with kv_heads.  Strides in elements, multiples of 8 (a head stride is not
+ * used with one head); the four base addresses 16-byte aligned.  lse: device, fp32
+ * [q_heads, total_q].  cu_q, cu_k: device, int32 [num_seqs + 1], not falling, within
+ * [0, total_q] and [0, total_k]: tokens before cu_q[0] or after cu_q[num_seqs] are in no
+ * sequence, and their rows of o and lse are left as they were.  A sequence whose entries fall
+ * or leave the buffers is skipped and reported through lva_device_error as
+ * LVA_ERR_INVALID_ARG (detail = the sequence).
+ *
+ * Keys outside a sequence never matter, whatever memory holds there.  Inside a sequence, a
+ * value that is not finite at a causally unseen key can reach the rows of the same tile of
+ * 128 rows (its weight there is zero, and zero times infinity is not).
+ *
+ * Errors: LVA_ERR_INVALID_ARG for null or misaligned pointers, bad strides or sizes, q_heads
+ * not a multiple of kv_heads, or a scale that is not positive and finite; LVA_ERR_UNSUPPORTED
+ * for d other than 64 and 128, more than 128 query heads per key/value head, totals of 2^31
+ * tokens, or more tiles than one launch covers.  num_seqs == 0 or total_q == 0 is a no-op.
+ */
+typedef struct {
+  int num_seqs;
+  int q_heads, kv_heads;       /* kv_heads divides q_heads */
+  int d;                       /* 64 or 128 */
+  int causal;
+  float scale;
+  int64_t total_q, total_k;    /* tokens of the buffers */
+  int64_t q_token_stride, q_head_stride;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t o_token_stride, o_head_stride;
+} lva_packed_params;
+
+lva_status lva_packed_attn(const lva_packed_params* params, const void* q, const void* k,
+                           const void* v, void* o, float* lse, const int32_t* cu_q,
+                           const int32_t* cu_k, cudaStream_t stream);
+
+/*
  * lva_device_error -- read and clear the current device's kernel error word.
  *
  * Synchronises `stream`, then stores in *status the first kernel-side fault recorded since
