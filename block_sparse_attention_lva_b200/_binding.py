@@ -62,6 +62,16 @@ class LvaPackedParams(ctypes.Structure):
                 ("o_token_stride", ctypes.c_int64), ("o_head_stride", ctypes.c_int64)]
 
 
+class LvaSharedPrefixParams(ctypes.Structure):
+    """Mirror of ``lva_shared_prefix_params``."""
+    _fields_ = [("B", ctypes.c_int), ("steps", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("d", ctypes.c_int), ("scale", ctypes.c_float), ("prefix_len", ctypes.c_int64),
+                ("capacity", ctypes.c_int64), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("o_token_stride", ctypes.c_int64), ("o_head_stride", ctypes.c_int64)]
+
+
 SIGNATURES = {
     "lva_status_string": (ctypes.c_char_p, [_c_int]),
     "lva_last_error_message": (ctypes.c_char_p, []),
@@ -92,6 +102,13 @@ SIGNATURES = {
                                      _vp, _c_int, _vp, _c_int, ctypes.POINTER(LvaHostStepBuffers), _c_int, _vp, _vp,
                                      _vp, ctypes.POINTER(ctypes.c_void_p)]),
     "lva_packed_attn": (_c_int, [ctypes.POINTER(LvaPackedParams), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "lva_shared_prefix_workspace_bytes": (_c_i64, [ctypes.POINTER(LvaSharedPrefixParams), _c_int]),
+    "lva_shared_prefix_attn": (_c_int, [ctypes.POINTER(LvaSharedPrefixParams), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                        _vp, _vp, _c_i64, _vp]),
+    "lva_append_cache": (_c_int, [_vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int,
+                                  _c_int, _c_i64, _c_int, _vp]),
+    "lva_evict_cache": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_i64, _c_int, _c_i64,
+                                 _c_i64, _c_i64, _vp]),
     "lva_device_error": (_c_int, [_vp, ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_int)]),
     "lva_selftest_wait": (_c_int, [_c_int, _vp]),
 }
@@ -478,6 +495,100 @@ def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = Tr
     _check(lib.lva_packed_attn(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_q),
                                _ptr(cu_k), ctypes.c_void_p(_stream(q.device))))
     return o, lse
+
+
+def lva_shared_prefix_workspace_bytes(B: int, steps: int, q_heads: int, kv_heads: int, d: int, prefix_len: int,
+                                      capacity: int, with_weight: bool = False) -> int:
+    """Workspace bytes of ``lva_shared_prefix_attn`` for these sizes (-1 for sizes it refuses)."""
+    p = LvaSharedPrefixParams(B, steps, q_heads, kv_heads, d, 1.0, prefix_len, capacity)
+    return lib.lva_shared_prefix_workspace_bytes(ctypes.byref(p), int(bool(with_weight)))
+
+
+def _steps_view(t, name: str, shape):
+    """``_heads_view`` of a [B, steps, heads, d] tensor whose tokens have one stride."""
+    _need(t is not None and tuple(t.shape) == shape, f"{name} must have shape {shape}")
+    B, steps, heads, d = shape
+    _need(B <= 1 or steps <= 1 or t.stride(0) == steps * t.stride(1), f"{name}: the tokens of a batch must have one stride")
+    # token b * steps + t at that many strides; a batch of single tokens has the batch's own
+    token = t.stride(0) if steps == 1 else t.stride(1)
+    return _heads_view(t.as_strided((B * steps, heads, d), (token, t.stride(2), t.stride(3))), name, (B * steps, heads, d))
+
+
+def lva_shared_prefix_attn(q, prefix_k, prefix_v, k_cache, v_cache, lens, o, lse, workspace, scale: float, weight=None):
+    """O, LSE of each sequence's step tokens over a shared key prefix and its own cache: q, o
+    [B, steps, Hq, d], prefix_k, prefix_v [Lp, Hkv, d] (or None), k_cache, v_cache
+    [B, Hkv, capacity, d], lens [B] (int32, the step's own tokens included), lse [B, Hq, steps]
+    (fp32), workspace (uint8, ``lva_shared_prefix_workspace_bytes``).  With ``weight``
+    ([B, Hkv, capacity] fp32) every cache key's attention probabilities are added to it."""
+    import torch
+    _need(q.dim() == 4 and k_cache.dim() == 4, "q must be [B, steps, heads, d], the caches [B, heads, capacity, d]")
+    B, steps, hq, d = q.shape
+    hk, cap = k_cache.shape[1], k_cache.shape[2]
+    qs, os = _steps_view(q, "q", (B, steps, hq, d)), _steps_view(o, "o", (B, steps, hq, d))
+    lp, ks, vs = 0, (0, 0), (0, 0)
+    if prefix_k is not None:
+        lp = prefix_k.shape[0]
+        ks, vs = _heads_view(prefix_k, "prefix_k", (lp, hk, d)), _heads_view(prefix_v, "prefix_v", (lp, hk, d))
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _cuda_tensor(t, name, torch.bfloat16)
+        _need(tuple(t.shape) == (B, hk, cap, d), f"{name} must have shape {(B, hk, cap, d)}")
+    _cuda_tensor(lens, "lens", torch.int32, B)
+    _cuda_tensor(lse, "lse", torch.float32, B * hq * steps)
+    if weight is not None:
+        _cuda_tensor(weight, "weight", torch.float32)
+        _need(tuple(weight.shape) == (B, hk, cap), f"weight must have shape {(B, hk, cap)}")
+    _cuda_tensor(workspace, "workspace")
+    p = LvaSharedPrefixParams(B, steps, hq, hk, d, scale, lp, cap, *qs, *ks, *vs, *os)
+    _check(lib.lva_shared_prefix_attn(ctypes.byref(p), _ptr(q), _ptr(prefix_k), _ptr(prefix_v), _ptr(k_cache),
+                                      _ptr(v_cache), _ptr(lens), _ptr(o), _ptr(lse), _ptr(weight), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(),
+                                      ctypes.c_void_p(_stream(q.device))))
+    return o, lse
+
+
+def lva_append_cache(k_new, v_new, k_cache, v_cache, weight, lens, lens_out):
+    """Put a step's tokens k_new, v_new [B, steps, Hkv, d] at place lens[b] of the caches
+    [B, Hkv, capacity, d], set their weight ([B, Hkv, capacity] or None) to 0 and
+    lens_out = lens + steps (lens_out may be lens)."""
+    import torch
+    _need(k_new.dim() == 4 and k_cache.dim() == 4, "k_new must be [B, steps, heads, d], the caches [B, heads, capacity, d]")
+    B, steps, hk, d = k_new.shape
+    cap = k_cache.shape[2]
+    ks, vs = _steps_view(k_new, "k_new", (B, steps, hk, d)), _steps_view(v_new, "v_new", (B, steps, hk, d))
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _cuda_tensor(t, name, torch.bfloat16)
+        _need(tuple(t.shape) == (B, hk, cap, d), f"{name} must have shape {(B, hk, cap, d)}")
+    if weight is not None:
+        _cuda_tensor(weight, "weight", torch.float32)
+        _need(tuple(weight.shape) == (B, hk, cap), f"weight must have shape {(B, hk, cap)}")
+    _cuda_tensor(lens, "lens", torch.int32, B)
+    _cuda_tensor(lens_out, "lens_out", torch.int32, B)
+    _check(lib.lva_append_cache(_ptr(k_new), _ptr(v_new), *ks, *vs, _ptr(k_cache), _ptr(v_cache), _ptr(weight), _ptr(lens),
+                                _ptr(lens_out), B, steps, hk, cap, d, ctypes.c_void_p(_stream(k_cache.device))))
+    return lens_out
+
+
+def lva_evict_cache(k_cache, v_cache, weight, lens, k_out, v_out, weight_out, lens_out, kept, budget: int, sinks: int = 0,
+                    recent: int = 0):
+    """Cut every cache with more than ``budget`` live entries back to its first ``sinks``, its
+    last ``recent`` and the entries of largest weight between them; ``kept``
+    [B, Hkv, budget] (int32) takes their old indices.  The outputs may be the inputs."""
+    import torch
+    _need(k_cache.dim() == 4, "the caches must be [B, heads, capacity, d]")
+    B, hk, cap, d = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("k_out", k_out), ("v_out", v_out)):
+        _cuda_tensor(t, name, torch.bfloat16)
+        _need(tuple(t.shape) == (B, hk, cap, d), f"{name} must have shape {(B, hk, cap, d)}")
+    for name, t in (("weight", weight), ("weight_out", weight_out)):
+        _cuda_tensor(t, name, torch.float32)
+        _need(tuple(t.shape) == (B, hk, cap), f"{name} must have shape {(B, hk, cap)}")
+    _cuda_tensor(lens, "lens", torch.int32, B)
+    _cuda_tensor(lens_out, "lens_out", torch.int32, B)
+    _cuda_tensor(kept, "kept", torch.int32, B * hk * max(0, int(budget)))
+    _check(lib.lva_evict_cache(_ptr(k_cache), _ptr(v_cache), _ptr(weight), _ptr(lens), _ptr(k_out), _ptr(v_out),
+                               _ptr(weight_out), _ptr(lens_out), _ptr(kept), B, hk, cap, d, int(budget), int(sinks),
+                               int(recent), ctypes.c_void_p(_stream(k_cache.device))))
+    return k_out, v_out, weight_out, lens_out, kept
 
 
 def lva_device_error(stream=None):

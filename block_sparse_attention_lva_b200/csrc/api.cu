@@ -476,6 +476,201 @@ lva_status lva_packed_attn(const lva_packed_params* p, const void* q, const void
   return ok();
 }
 
+// Parts of the prefix: as many as shorten the longest CTA's walk.  With c = items * parts CTAs
+// on 148 SMs the pass takes about ceil(c / 148) * (ceil(blocks / parts) + 2) block times, the 2
+// for a part's start and end; parts past 32 would cost more in joining than they gain.
+static int prefix_parts(const lva_shared_prefix_params* p) {
+  if (p->prefix_len == 0) return 0;
+  const int tok = 128 / (p->q_heads / p->kv_heads);
+  const int64_t items = (int64_t(p->B) * p->steps + tok - 1) / tok * p->kv_heads;
+  const int64_t blocks = (p->prefix_len + 127) / 128;
+  int best = 1;
+  int64_t best_cost = 0;
+  for (int s = 1; s <= 32 && s <= blocks; ++s) {
+    const int64_t cost = (items * s + 147) / 148 * ((blocks + s - 1) / s + 2);
+    if (s == 1 || cost < best_cost) { best = s; best_cost = cost; }
+  }
+  return best;
+}
+
+// Byte offsets of the workspace's pieces (256-byte steps).
+struct PrefixWorkspace {
+  int parts;
+  int64_t part_o, part_lse, own_o, own_lse, scores, score_stride, bytes;
+};
+
+static lva_status prefix_plan(const lva_shared_prefix_params* p, bool with_weight, PrefixWorkspace* w) {
+  if (p == nullptr) return fail(LVA_ERR_INVALID_ARG, "shared_prefix: null params");
+  const lva_status s = check_heads("shared_prefix", p->q_heads, p->kv_heads, p->d, p->scale);
+  if (s != LVA_OK) return s;
+  if (p->B < 0 || p->steps < 1) return fail(LVA_ERR_INVALID_ARG, "shared_prefix: need B >= 0 and steps >= 1");
+  if (p->prefix_len < 0 || p->capacity < 0)
+    return fail(LVA_ERR_INVALID_ARG, "shared_prefix: prefix_len and capacity must be >= 0");
+  const int64_t group = p->q_heads / p->kv_heads, rows = p->steps * group;
+  if (rows > kCacheMaxRows)
+    return fail(LVA_ERR_UNSUPPORTED, "shared_prefix: steps * q_heads / kv_heads must be <= %d", kCacheMaxRows);
+  const int64_t most = int64_t(1) << 31;
+  if (p->prefix_len >= most || p->capacity >= most)
+    return fail(LVA_ERR_UNSUPPORTED, "shared_prefix: prefix_len and capacity must be < 2^31");
+  const int64_t planes = int64_t(p->B) * p->kv_heads;
+  const int64_t chunks = with_weight ? p->capacity / 512 + 1 : 0;
+  if (planes >= most || planes * rows >= most || (p->capacity > 0 && planes >= most / p->capacity) ||
+      planes * rows / 4 + 1 + planes * chunks >= most)
+    return fail(LVA_ERR_UNSUPPORTED, "shared_prefix: B * kv_heads * capacity and B * steps * q_heads must be < 2^31");
+  auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  w->parts = prefix_parts(p);
+  const int64_t part_rows = int64_t(w->parts) * planes * rows;
+  const int64_t own_rows = p->capacity > 0 ? (planes + kCacheWorkers) * rows : 0;
+  w->score_stride = (p->capacity + 63) / 64 * 64;
+  w->part_o = 0;
+  w->part_lse = w->part_o + up(part_rows * p->d * 4);
+  w->own_o = w->part_lse + up(part_rows * 4);
+  w->own_lse = w->own_o + up(own_rows * p->d * 4);
+  w->scores = w->own_lse + up(own_rows * 4);
+  w->bytes = w->scores + (with_weight ? up(planes * rows * w->score_stride * 4) : 0);
+  return LVA_OK;
+}
+
+int64_t lva_shared_prefix_workspace_bytes(const lva_shared_prefix_params* p, int with_weight) {
+  PrefixWorkspace w;
+  return prefix_plan(p, with_weight != 0, &w) == LVA_OK ? w.bytes : -1;
+}
+
+lva_status lva_shared_prefix_attn(const lva_shared_prefix_params* p, const void* q, const void* prefix_k,
+                                  const void* prefix_v, const void* k_cache, const void* v_cache,
+                                  const int32_t* lens, void* o, float* lse, float* weight, void* workspace,
+                                  int64_t workspace_bytes, cudaStream_t stream) {
+  PrefixWorkspace w;
+  const lva_status s = prefix_plan(p, weight != nullptr, &w);
+  if (s != LVA_OK) return s;
+  if (!view_ok(p->q_token_stride, p->q_head_stride, p->q_heads, p->d) ||
+      !view_ok(p->o_token_stride, p->o_head_stride, p->q_heads, p->d) ||
+      (p->prefix_len > 0 && (!view_ok(p->k_token_stride, p->k_head_stride, p->kv_heads, p->d) ||
+                             !view_ok(p->v_token_stride, p->v_head_stride, p->kv_heads, p->d))))
+    return fail(LVA_ERR_INVALID_ARG, "shared_prefix: strides must be multiples of 8 elements, at least d");
+  if (p->B == 0) return ok();
+  if (!q || !o || !lse || (p->prefix_len > 0 && (!prefix_k || !prefix_v)) ||
+      (p->capacity > 0 && (!k_cache || !v_cache || !lens)) || (w.bytes > 0 && !workspace))
+    return fail(LVA_ERR_INVALID_ARG, "shared_prefix: null pointer");
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(prefix_k, 16) || !aligned(prefix_v, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(workspace, 16))
+    return fail(LVA_ERR_INVALID_ARG, "shared_prefix: q, k, v, o, caches and workspace must be 16-byte aligned");
+  if (!aligned(lens, 4) || !aligned(lse, 4) || !aligned(weight, 4))
+    return fail(LVA_ERR_INVALID_ARG, "shared_prefix: lens, lse, weight must be 4-byte aligned");
+  if (workspace_bytes < w.bytes)
+    return fail(LVA_ERR_CAPACITY, "shared_prefix: workspace_bytes %lld < %lld", (long long)workspace_bytes,
+                (long long)w.bytes);
+  int* err = device_error_word();
+  if (err == nullptr) return fail(LVA_ERR_CUDA, "shared_prefix: cannot locate the device error word");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* part_o = reinterpret_cast<float*>(ws + w.part_o);
+  float* part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  const char* why = "launch";
+  if (w.parts > 0) {
+    PackedArgs a{q, prefix_k, prefix_v, nullptr, nullptr, 1, p->q_heads, p->kv_heads, p->d,
+                 int64_t(p->B) * p->steps, p->prefix_len,
+                 p->q_token_stride, p->q_head_stride, p->k_token_stride, p->k_head_stride,
+                 p->v_token_stride, p->v_head_stride, 0, 0, nullptr, nullptr, 0, p->scale,
+                 w.parts, part_o, part_lse, err};
+    const cudaError_t e = launch_packed(a, stream, &why);
+    if (e != cudaSuccess) return fail(LVA_ERR_CUDA, "shared_prefix: %s: %s", why, cudaGetErrorString(e));
+  }
+  CacheAttnArgs c{q, k_cache, v_cache, lens, o, lse, p->capacity > 0 ? weight : nullptr, p->B, p->steps, p->q_heads,
+                  p->kv_heads, p->d, p->prefix_len, p->capacity, p->q_token_stride, p->q_head_stride,
+                  p->o_token_stride, p->o_head_stride, p->scale, w.parts, part_o, part_lse,
+                  reinterpret_cast<float*>(ws + w.own_o), reinterpret_cast<float*>(ws + w.own_lse),
+                  weight != nullptr ? reinterpret_cast<float*>(ws + w.scores) : nullptr, w.score_stride, err};
+  if (p->capacity > 0) {
+    const cudaError_t e = launch_cache_attn(c, stream, &why);
+    if (e != cudaSuccess) return fail(LVA_ERR_CUDA, "shared_prefix: %s: %s", why, cudaGetErrorString(e));
+  }
+  return from_cuda(launch_cache_join(c, stream), "shared_prefix join launch");
+}
+
+// Sizes of [B, kv_heads, capacity, d] caches.
+static lva_status check_cache(const char* fn, int B, int kv_heads, int64_t capacity, int d) {
+  if (B < 0 || kv_heads < 1 || capacity < 0)
+    return fail(LVA_ERR_INVALID_ARG, "%s: need B >= 0, kv_heads >= 1, capacity >= 0", fn);
+  if (d != 64 && d != 128) return fail(LVA_ERR_UNSUPPORTED, "%s: head dim must be 64 or 128", fn);
+  const int64_t most = int64_t(1) << 31;
+  const int64_t planes = int64_t(B) * kv_heads;
+  if (planes >= most || capacity >= most || (planes > 0 && capacity >= (int64_t(1) << 40) / planes))
+    return fail(LVA_ERR_UNSUPPORTED, "%s: B * kv_heads and capacity must be < 2^31, their product < 2^40", fn);
+  return LVA_OK;
+}
+
+lva_status lva_append_cache(const void* k_new, const void* v_new, int64_t k_token_stride, int64_t k_head_stride,
+                            int64_t v_token_stride, int64_t v_head_stride, void* k_cache, void* v_cache,
+                            float* weight, const int32_t* lens, int32_t* lens_out, int B, int steps, int kv_heads,
+                            int64_t capacity, int d, cudaStream_t stream) {
+  const lva_status s = check_cache("append", B, kv_heads, capacity, d);
+  if (s != LVA_OK) return s;
+  if (steps < 0) return fail(LVA_ERR_INVALID_ARG, "append: steps must be >= 0");
+  if (!view_ok(k_token_stride, k_head_stride, kv_heads, d) || !view_ok(v_token_stride, v_head_stride, kv_heads, d))
+    return fail(LVA_ERR_INVALID_ARG, "append: strides must be multiples of 8 elements, at least d");
+  const int64_t most = int64_t(1) << 31;
+  const int64_t units = int64_t(kv_heads) * steps;               // rows of one sequence, K or V
+  if (units >= most / 32 || units * 32 / 2048 + 1 >= most / (B > 0 ? B : 1))
+    return fail(LVA_ERR_UNSUPPORTED, "append: too many rows for one launch");
+  if (B == 0) return ok();
+  if (!lens || !lens_out || (steps > 0 && (!k_new || !v_new || (capacity > 0 && (!k_cache || !v_cache)))))
+    return fail(LVA_ERR_INVALID_ARG, "append: null pointer");
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+    return fail(LVA_ERR_INVALID_ARG, "append: rows and caches must be 16-byte aligned");
+  if (!aligned(weight, 4) || !aligned(lens, 4) || !aligned(lens_out, 4))
+    return fail(LVA_ERR_INVALID_ARG, "append: weight and lens must be 4-byte aligned");
+  int* err = device_error_word();
+  if (err == nullptr) return fail(LVA_ERR_CUDA, "append: cannot locate the device error word");
+  AppendArgs a{k_new, v_new, k_cache, v_cache, weight, lens, lens_out, B, steps, kv_heads, d, capacity,
+               k_token_stride, k_head_stride, v_token_stride, v_head_stride, err};
+  return from_cuda(launch_append(a, stream), "append launch");
+}
+
+// Whether [a, a + n) and [b, b + n) share a byte.
+static bool overlap(const void* a, const void* b, int64_t n) {
+  const intptr_t x = reinterpret_cast<intptr_t>(a), y = reinterpret_cast<intptr_t>(b);
+  return x < y + n && y < x + n;
+}
+
+lva_status lva_evict_cache(const void* k_cache, const void* v_cache, const float* weight, const int32_t* lens,
+                           void* k_out, void* v_out, float* weight_out, int32_t* lens_out, int32_t* kept, int B,
+                           int kv_heads, int64_t capacity, int d, int64_t budget, int64_t sinks, int64_t recent,
+                           cudaStream_t stream) {
+  const lva_status s = check_cache("evict", B, kv_heads, capacity, d);
+  if (s != LVA_OK) return s;
+  if (budget < 1 || budget > capacity) return fail(LVA_ERR_INVALID_ARG, "evict: need 1 <= budget <= capacity");
+  if (sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks)
+    return fail(LVA_ERR_INVALID_ARG, "evict: need sinks, recent >= 0 and sinks + recent <= budget");
+  const int64_t planes = int64_t(B) * kv_heads;
+  if (planes * 33 >= (int64_t(1) << 31) || (budget + 63) / 64 >= (int64_t(1) << 31) / (planes > 0 ? planes : 1))
+    return fail(LVA_ERR_UNSUPPORTED, "evict: too many rows for one launch");
+  if (B == 0) return ok();
+  if (!k_cache || !v_cache || !weight || !lens || !k_out || !v_out || !weight_out || !lens_out || !kept)
+    return fail(LVA_ERR_INVALID_ARG, "evict: null pointer");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(LVA_ERR_INVALID_ARG, "evict: caches must be 16-byte aligned");
+  if (!aligned(weight, 4) || !aligned(weight_out, 4) || !aligned(lens, 4) || !aligned(lens_out, 4) || !aligned(kept, 4))
+    return fail(LVA_ERR_INVALID_ARG, "evict: weight, lens and kept must be 4-byte aligned");
+  const int64_t bytes = planes * capacity * d * 2;
+  const bool in_k = k_out == k_cache, in_v = v_out == v_cache, in_w = weight_out == weight;
+  if (in_k != in_v || in_k != in_w)
+    return fail(LVA_ERR_INVALID_ARG, "evict: k, v and weight must be in place together or not at all");
+  if (!in_k) {
+    const void* in[2] = {k_cache, v_cache};
+    for (const void* x : in)
+      if (overlap(x, k_out, bytes) || overlap(x, v_out, bytes))
+        return fail(LVA_ERR_INVALID_ARG, "evict: outputs must not overlap the caches");
+    if (overlap(weight, weight_out, planes * capacity * 4))
+      return fail(LVA_ERR_INVALID_ARG, "evict: weight_out must not overlap weight");
+  }
+  if (overlap(k_out, v_out, bytes)) return fail(LVA_ERR_INVALID_ARG, "evict: k and v must not overlap");
+  int* err = device_error_word();
+  if (err == nullptr) return fail(LVA_ERR_CUDA, "evict: cannot locate the device error word");
+  EvictArgs a{k_cache, v_cache, weight, lens, k_out, v_out, weight_out, lens_out, kept, B, kv_heads, d,
+              capacity, budget, sinks, recent, err};
+  return from_cuda(launch_evict(a, stream), "evict launch");
+}
+
 lva_status lva_selftest_wait(int mode, cudaStream_t stream) {
   if (mode < 0 || mode > 2) return fail(LVA_ERR_INVALID_ARG, "selftest_wait: mode must be 0, 1 or 2");
   int* err = device_error_word();

@@ -517,6 +517,113 @@ lva_status lva_packed_attn(const lva_packed_params* params, const void* q, const
                            const int32_t* cu_k, cudaStream_t stream);
 
 /*
+ * lva_shared_prefix_attn -- attention of a step's tokens over a key prefix that the whole
+ * batch shares and over each sequence's own cache.
+ *
+ * Several samples rolled out from one prompt or context: its keys and values (B times the
+ * same) are read once for all of them, next to caches that grow apart.  The pages have no
+ * counterpart.
+ *
+ * q, o: device, bf16 [B, steps, q_heads, d] with element (token b*steps + t, head h, e) at
+ * (b*steps + t) * token_stride + h * head_stride + e.  prefix_k, prefix_v: device, bf16
+ * [prefix_len, kv_heads, d] with their own token and head strides (k and v of
+ * lva_packed_attn's layout).  k_cache, v_cache: device, bf16 [B, kv_heads, capacity, d],
+ * contiguous.  lens: device, int32 [B]: live entries of each cache, the keys of this call's
+ * `steps` tokens among them (lva_append_cache puts them there).  Query head h reads
+ * key/value head h / (q_heads/kv_heads).  Token t of sequence b sees every prefix key and
+ * the cache keys c <= lens[b] - steps + t; with
+ *   LSE = ln sum_c exp(scale <q, k_c>),  O = sum_c exp(scale <q, k_c> - LSE) v_c
+ * over both.  lse: device, fp32 [B, q_heads, steps].  A token that sees no key gets O = 0 and
+ * LSE = -inf.  Cache entries from lens[b] on never matter, whatever memory holds there.
+ *
+ * weight: NULL, or device, fp32 [B, kv_heads, capacity], to which every live cache key's
+ * attention probabilities, summed over the step's tokens and the heads of its group, are
+ * added (what lva_evict_cache ranks by).  Additions have a fixed order.
+ *
+ * workspace: device, 16-byte aligned, at least lva_shared_prefix_workspace_bytes bytes, its
+ * contents without meaning between calls; calls (and captured graphs) that may run at the
+ * same time need one each.  The size depends on the params and on whether weight is given,
+ * not on lens.  (-1 for bad params.)
+ *
+ * A length outside [0, capacity] counts as 0 and is reported through lva_device_error as
+ * LVA_ERR_INVALID_ARG (detail = the sequence).
+ * Errors: LVA_ERR_INVALID_ARG for null or misaligned pointers, bad strides or sizes, or a
+ * scale that is not positive and finite; LVA_ERR_UNSUPPORTED for d other than 64 and 128,
+ * more than 64 rows (steps * q_heads / kv_heads), or sizes past 2^31 rows;
+ * LVA_ERR_CAPACITY for a small workspace.  B == 0 is a no-op.
+ */
+typedef struct {
+  int B, steps;                /* sequences, query tokens per sequence (>= 1) */
+  int q_heads, kv_heads;       /* kv_heads divides q_heads */
+  int d;                       /* 64 or 128 */
+  float scale;
+  int64_t prefix_len;          /* >= 0 */
+  int64_t capacity;            /* entries a cache holds, >= 0 */
+  int64_t q_token_stride, q_head_stride;
+  int64_t k_token_stride, k_head_stride;   /* prefix_k */
+  int64_t v_token_stride, v_head_stride;   /* prefix_v */
+  int64_t o_token_stride, o_head_stride;
+} lva_shared_prefix_params;
+
+int64_t lva_shared_prefix_workspace_bytes(const lva_shared_prefix_params* params, int with_weight);
+
+lva_status lva_shared_prefix_attn(const lva_shared_prefix_params* params, const void* q,
+                                  const void* prefix_k, const void* prefix_v, const void* k_cache,
+                                  const void* v_cache, const int32_t* lens, void* o, float* lse,
+                                  float* weight, void* workspace, int64_t workspace_bytes,
+                                  cudaStream_t stream);
+
+/*
+ * lva_append_cache -- put a step's tokens into the caches.
+ *
+ * Row lens[b] + t of every head of sequence b's caches takes token t of k_new, v_new, its
+ * weight (weight: NULL or fp32 [B, kv_heads, capacity]) becomes 0, and lens_out[b] =
+ * lens[b] + steps.  lens_out may be lens.  A sequence whose cache is too full (or whose
+ * length is negative) is left as it is, lens_out[b] = lens[b], and reported through
+ * lva_device_error as LVA_ERR_CAPACITY (detail = the sequence).
+ *
+ * k_new, v_new: device, bf16, element (token b*steps + t, head h, e) at
+ * (b*steps + t) * token_stride + h * head_stride + e, strides in elements, multiples of 8;
+ * k_cache, v_cache: device, bf16 [B, kv_heads, capacity, d]; addresses 16-byte aligned.
+ * Errors: LVA_ERR_INVALID_ARG for null or misaligned pointers, bad strides or sizes;
+ * LVA_ERR_UNSUPPORTED for d other than 64 and 128 or sizes past one launch.  B == 0 or
+ * steps == 0 copies nothing (lens_out still becomes lens).
+ */
+lva_status lva_append_cache(const void* k_new, const void* v_new, int64_t k_token_stride,
+                            int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                            void* k_cache, void* v_cache, float* weight, const int32_t* lens,
+                            int32_t* lens_out, int B, int steps, int kv_heads, int64_t capacity, int d,
+                            cudaStream_t stream);
+
+/*
+ * lva_evict_cache -- cut caches back to a budget by accumulated attention weight.
+ *
+ * For every sequence b with n = lens[b] > budget live entries, each key/value head keeps its
+ * first `sinks` and last `recent` entries and, of the others, the budget - sinks - recent of
+ * largest weight (ties to the lower index; NaN ranks below every number), in their order;
+ * other sequences keep everything.  The counterpart, for single cached tokens, of
+ * lva_block_energy and lva_select_blocks.
+ *
+ * The kept rows, weights and lengths go to k_out, v_out, weight_out (shaped like k_cache,
+ * v_cache, weight) and lens_out; rows past a sequence's new length are left as they were.
+ * In place (k_out == k_cache, v_out == v_cache, weight_out == weight, all three or none) rows
+ * move down within the caches; otherwise outputs and inputs must not overlap.  lens_out may be
+ * lens either way.  kept: device, int32 [B, kv_heads, budget]: the old index of every kept
+ * row (identity and then -1 for a sequence below its budget).
+ *
+ * A length outside [0, capacity] is reported through lva_device_error as LVA_ERR_INVALID_ARG
+ * (detail = the sequence); that sequence is left as it is (kept = -1).
+ * Errors: LVA_ERR_INVALID_ARG for null or misaligned pointers (caches 16 bytes), overlapping
+ * or half in-place outputs, budget < 1, budget > capacity, or sinks + recent > budget;
+ * LVA_ERR_UNSUPPORTED for d other than 64 and 128 or sizes past one launch.  B == 0 is a
+ * no-op.
+ */
+lva_status lva_evict_cache(const void* k_cache, const void* v_cache, const float* weight,
+                           const int32_t* lens, void* k_out, void* v_out, float* weight_out,
+                           int32_t* lens_out, int32_t* kept, int B, int kv_heads, int64_t capacity,
+                           int d, int64_t budget, int64_t sinks, int64_t recent, cudaStream_t stream);
+
+/*
  * lva_device_error -- read and clear the current device's kernel error word.
  *
  * Synchronises `stream`, then stores in *status the first kernel-side fault recorded since
