@@ -11,6 +11,8 @@ import ctypes
 import os
 from dataclasses import dataclass
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblva.so")
 
@@ -461,39 +463,108 @@ def lva_layer_step_host(qkv_host, o_host, lse_host, shape: LvaLayerShape, params
     return done.value
 
 
-def _heads_view(t, name: str, shape):
+# The context calls below are short, and a step of a rollout makes several of them: their
+# checks build no message and convert no argument unless one fails, and read the stream
+# without making a Stream object.
+
+
+def _refuse(msg: str):
+    raise ValueError(msg)
+
+
+def _on_device(t, name: str, dtype, cur: int):
+    if t is None or not t.is_cuda:
+        _refuse(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        _refuse(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != cur:
+        _refuse(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{cur}")
+
+
+def _heads_view(t, name: str, shape, cur: int):
     """Checks a bf16 CUDA tensor [tokens, heads, d] on the current device whose rows are
     contiguous (token and head strides are free: slices of a fused projection serve as they
     are); returns (token stride, head stride)."""
-    import torch
-    _need(t is not None and t.is_cuda, f"{name} must be a CUDA tensor")
-    _need(t.dtype == torch.bfloat16, f"{name} must be torch.bfloat16, got {t.dtype}")
-    current = torch.cuda.current_device()
-    _need(t.device.index == current, f"{name} is on cuda:{t.device.index}, the current device is cuda:{current}")
-    _need(tuple(t.shape) == shape, f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    _on_device(t, name, torch.bfloat16, cur)
+    if t.shape != shape:
+        _refuse(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     st, sh, se = t.stride()
-    _need(se == 1, f"{name} must be contiguous in its last dimension")
-    # the stride of a dimension of one element is never walked, whatever the view says
-    return (st if shape[0] > 1 else shape[1] * max(sh, shape[2]) if shape[1] > 1 else shape[2]), sh
+    return _strides(name, st, sh, se, *shape)
+
+
+def _strides(name: str, st: int, sh: int, se: int, tokens: int, heads: int, d: int):
+    if se != 1:
+        _refuse(f"{name} must be contiguous in its last dimension")
+    if tokens <= 1:      # the stride of a dimension of one element is never walked, whatever the view says
+        st = d if heads <= 1 else heads * max(sh, d)
+    return st, sh
+
+
+def _steps_view(t, name: str, shape, cur: int):
+    """``_heads_view`` of a [B, steps, heads, d] tensor whose tokens have one stride."""
+    _on_device(t, name, torch.bfloat16, cur)
+    if t.shape != shape:
+        _refuse(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    B, steps, heads, d = shape
+    sb, st, sh, se = t.stride()
+    if steps == 1:       # a batch of single tokens has the batch's own stride
+        st = sb
+    elif B > 1 and sb != steps * st:
+        _refuse(f"{name}: the tokens of a batch must have one stride")
+    return _strides(name, st, sh, se, B * steps, heads, d)
+
+
+def _whole(t, name: str, dtype, shape, cur: int):
+    """Address of a contiguous CUDA tensor of exactly this shape on the current device."""
+    _on_device(t, name, dtype, cur)
+    if t.shape != shape:
+        _refuse(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        _refuse(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _at_least(t, name: str, dtype, numel: int, cur: int):
+    """Address of a contiguous CUDA tensor with ``numel`` elements or more."""
+    _on_device(t, name, dtype, cur)
+    if not t.is_contiguous():
+        _refuse(f"{name} must be contiguous")
+    if t.numel() < numel:
+        _refuse(f"{name} has {t.numel()} elements, needs {numel}")
+    return t.data_ptr()
+
+
+def _device_of(t, name: str) -> int:
+    """The current device, for a call whose first tensor is ``t``."""
+    if t is None or not t.is_cuda:
+        _refuse(f"{name} must be a CUDA tensor")
+    return torch.cuda.current_device()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = True):
     """O, LSE of attention over packed sequences: q, o [total_q, Hq, d], k, v [total_k, Hkv, d]
     (bf16, rows contiguous, token and head strides free), lse [Hq, total_q] (fp32), cu_q and
     cu_k [sequences + 1] (int32, device).  Causal: a sequence's last query sees all its keys."""
-    import torch
-    _need(q.dim() == 3 and k.dim() == 3, "q and k must be [tokens, heads, d]")
-    tq, hq, d = q.shape
+    cur = _device_of(q, "q")
+    if q.dim() != 3 or k.dim() != 3:
+        _refuse("q and k must be [tokens, heads, d]")
+    qshape = q.shape
+    tq, hq, d = qshape
     tk, hk = k.shape[:2]
-    qs, ks = _heads_view(q, "q", (tq, hq, d)), _heads_view(k, "k", (tk, hk, d))
-    vs, os = _heads_view(v, "v", (tk, hk, d)), _heads_view(o, "o", (tq, hq, d))
-    _cuda_tensor(lse, "lse", torch.float32, hq * tq)
-    _cuda_tensor(cu_q, "cu_q", torch.int32, 1)
-    _cuda_tensor(cu_k, "cu_k", torch.int32, cu_q.numel())
-    _need(cu_q.numel() == cu_k.numel(), "cu_q and cu_k must have the same number of entries")
-    p = LvaPackedParams(cu_q.numel() - 1, hq, hk, d, int(bool(causal)), scale, tq, tk, *qs, *ks, *vs, *os)
-    _check(lib.lva_packed_attn(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_q),
-                               _ptr(cu_k), ctypes.c_void_p(_stream(q.device))))
+    kshape = (tk, hk, d)
+    p = LvaPackedParams(cu_q.numel() - 1, hq, hk, d, 1 if causal else 0, scale, tq, tk,
+                        *_heads_view(q, "q", qshape, cur), *_heads_view(k, "k", kshape, cur),
+                        *_heads_view(v, "v", kshape, cur), *_heads_view(o, "o", qshape, cur))
+    n = p.num_seqs + 1
+    if n < 1:
+        _refuse("cu_q must have at least one entry")
+    _check(lib.lva_packed_attn(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                               _whole(lse, "lse", torch.float32, (hq, tq), cur), _whole(cu_q, "cu_q", torch.int32, (n,), cur),
+                               _whole(cu_k, "cu_k", torch.int32, (n,), cur), _raw_stream(cur)))
     return o, lse
 
 
@@ -501,17 +572,7 @@ def lva_shared_prefix_workspace_bytes(B: int, steps: int, q_heads: int, kv_heads
                                       capacity: int, with_weight: bool = False) -> int:
     """Workspace bytes of ``lva_shared_prefix_attn`` for these sizes (-1 for sizes it refuses)."""
     p = LvaSharedPrefixParams(B, steps, q_heads, kv_heads, d, 1.0, prefix_len, capacity)
-    return lib.lva_shared_prefix_workspace_bytes(ctypes.byref(p), int(bool(with_weight)))
-
-
-def _steps_view(t, name: str, shape):
-    """``_heads_view`` of a [B, steps, heads, d] tensor whose tokens have one stride."""
-    _need(t is not None and tuple(t.shape) == shape, f"{name} must have shape {shape}")
-    B, steps, heads, d = shape
-    _need(B <= 1 or steps <= 1 or t.stride(0) == steps * t.stride(1), f"{name}: the tokens of a batch must have one stride")
-    # token b * steps + t at that many strides; a batch of single tokens has the batch's own
-    token = t.stride(0) if steps == 1 else t.stride(1)
-    return _heads_view(t.as_strided((B * steps, heads, d), (token, t.stride(2), t.stride(3))), name, (B * steps, heads, d))
+    return lib.lva_shared_prefix_workspace_bytes(p, 1 if with_weight else 0)
 
 
 def lva_shared_prefix_attn(q, prefix_k, prefix_v, k_cache, v_cache, lens, o, lse, workspace, scale: float, weight=None):
@@ -520,29 +581,27 @@ def lva_shared_prefix_attn(q, prefix_k, prefix_v, k_cache, v_cache, lens, o, lse
     [B, Hkv, capacity, d], lens [B] (int32, the step's own tokens included), lse [B, Hq, steps]
     (fp32), workspace (uint8, ``lva_shared_prefix_workspace_bytes``).  With ``weight``
     ([B, Hkv, capacity] fp32) every cache key's attention probabilities are added to it."""
-    import torch
-    _need(q.dim() == 4 and k_cache.dim() == 4, "q must be [B, steps, heads, d], the caches [B, heads, capacity, d]")
-    B, steps, hq, d = q.shape
-    hk, cap = k_cache.shape[1], k_cache.shape[2]
-    qs, os = _steps_view(q, "q", (B, steps, hq, d)), _steps_view(o, "o", (B, steps, hq, d))
-    lp, ks, vs = 0, (0, 0), (0, 0)
+    cur = _device_of(q, "q")
+    if q.dim() != 4 or k_cache.dim() != 4:
+        _refuse("q must be [B, steps, heads, d], the caches [B, heads, capacity, d]")
+    qshape = q.shape
+    B, steps, hq, d = qshape
+    hk, cap = k_cache.shape[1:3]
+    cshape = (B, hk, cap, d)
+    lp, ks, vs, pk, pv = 0, (0, 0), (0, 0), None, None
     if prefix_k is not None:
         lp = prefix_k.shape[0]
-        ks, vs = _heads_view(prefix_k, "prefix_k", (lp, hk, d)), _heads_view(prefix_v, "prefix_v", (lp, hk, d))
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _cuda_tensor(t, name, torch.bfloat16)
-        _need(tuple(t.shape) == (B, hk, cap, d), f"{name} must have shape {(B, hk, cap, d)}")
-    _cuda_tensor(lens, "lens", torch.int32, B)
-    _cuda_tensor(lse, "lse", torch.float32, B * hq * steps)
-    if weight is not None:
-        _cuda_tensor(weight, "weight", torch.float32)
-        _need(tuple(weight.shape) == (B, hk, cap), f"weight must have shape {(B, hk, cap)}")
-    _cuda_tensor(workspace, "workspace")
-    p = LvaSharedPrefixParams(B, steps, hq, hk, d, scale, lp, cap, *qs, *ks, *vs, *os)
-    _check(lib.lva_shared_prefix_attn(ctypes.byref(p), _ptr(q), _ptr(prefix_k), _ptr(prefix_v), _ptr(k_cache),
-                                      _ptr(v_cache), _ptr(lens), _ptr(o), _ptr(lse), _ptr(weight), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(),
-                                      ctypes.c_void_p(_stream(q.device))))
+        pshape = (lp, hk, d)
+        ks, vs = _heads_view(prefix_k, "prefix_k", pshape, cur), _heads_view(prefix_v, "prefix_v", pshape, cur)
+        pk, pv = prefix_k.data_ptr(), prefix_v.data_ptr()
+    p = LvaSharedPrefixParams(B, steps, hq, hk, d, scale, lp, cap, *_steps_view(q, "q", qshape, cur), *ks, *vs,
+                              *_steps_view(o, "o", qshape, cur))
+    _check(lib.lva_shared_prefix_attn(
+        p, q.data_ptr(), pk, pv, _whole(k_cache, "k_cache", torch.bfloat16, cshape, cur),
+        _whole(v_cache, "v_cache", torch.bfloat16, cshape, cur), _whole(lens, "lens", torch.int32, (B,), cur), o.data_ptr(),
+        _whole(lse, "lse", torch.float32, (B, hq, steps), cur),
+        None if weight is None else _whole(weight, "weight", torch.float32, cshape[:3], cur),
+        _at_least(workspace, "workspace", torch.uint8, 0, cur), workspace.numel(), _raw_stream(cur)))
     return o, lse
 
 
@@ -550,21 +609,20 @@ def lva_append_cache(k_new, v_new, k_cache, v_cache, weight, lens, lens_out):
     """Put a step's tokens k_new, v_new [B, steps, Hkv, d] at place lens[b] of the caches
     [B, Hkv, capacity, d], set their weight ([B, Hkv, capacity] or None) to 0 and
     lens_out = lens + steps (lens_out may be lens)."""
-    import torch
-    _need(k_new.dim() == 4 and k_cache.dim() == 4, "k_new must be [B, steps, heads, d], the caches [B, heads, capacity, d]")
-    B, steps, hk, d = k_new.shape
+    cur = _device_of(k_new, "k_new")
+    if k_new.dim() != 4 or k_cache.dim() != 4:
+        _refuse("k_new must be [B, steps, heads, d], the caches [B, heads, capacity, d]")
+    shape = k_new.shape
+    B, steps, hk, d = shape
     cap = k_cache.shape[2]
-    ks, vs = _steps_view(k_new, "k_new", (B, steps, hk, d)), _steps_view(v_new, "v_new", (B, steps, hk, d))
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _cuda_tensor(t, name, torch.bfloat16)
-        _need(tuple(t.shape) == (B, hk, cap, d), f"{name} must have shape {(B, hk, cap, d)}")
-    if weight is not None:
-        _cuda_tensor(weight, "weight", torch.float32)
-        _need(tuple(weight.shape) == (B, hk, cap), f"weight must have shape {(B, hk, cap)}")
-    _cuda_tensor(lens, "lens", torch.int32, B)
-    _cuda_tensor(lens_out, "lens_out", torch.int32, B)
-    _check(lib.lva_append_cache(_ptr(k_new), _ptr(v_new), *ks, *vs, _ptr(k_cache), _ptr(v_cache), _ptr(weight), _ptr(lens),
-                                _ptr(lens_out), B, steps, hk, cap, d, ctypes.c_void_p(_stream(k_cache.device))))
+    cshape = (B, hk, cap, d)
+    ks, vs = _steps_view(k_new, "k_new", shape, cur), _steps_view(v_new, "v_new", shape, cur)
+    _check(lib.lva_append_cache(
+        k_new.data_ptr(), v_new.data_ptr(), *ks, *vs, _whole(k_cache, "k_cache", torch.bfloat16, cshape, cur),
+        _whole(v_cache, "v_cache", torch.bfloat16, cshape, cur),
+        None if weight is None else _whole(weight, "weight", torch.float32, cshape[:3], cur),
+        _whole(lens, "lens", torch.int32, (B,), cur), _whole(lens_out, "lens_out", torch.int32, (B,), cur),
+        B, steps, hk, cap, d, _raw_stream(cur)))
     return lens_out
 
 
@@ -573,21 +631,19 @@ def lva_evict_cache(k_cache, v_cache, weight, lens, k_out, v_out, weight_out, le
     """Cut every cache with more than ``budget`` live entries back to its first ``sinks``, its
     last ``recent`` and the entries of largest weight between them; ``kept``
     [B, Hkv, budget] (int32) takes their old indices.  The outputs may be the inputs."""
-    import torch
-    _need(k_cache.dim() == 4, "the caches must be [B, heads, capacity, d]")
-    B, hk, cap, d = k_cache.shape
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("k_out", k_out), ("v_out", v_out)):
-        _cuda_tensor(t, name, torch.bfloat16)
-        _need(tuple(t.shape) == (B, hk, cap, d), f"{name} must have shape {(B, hk, cap, d)}")
-    for name, t in (("weight", weight), ("weight_out", weight_out)):
-        _cuda_tensor(t, name, torch.float32)
-        _need(tuple(t.shape) == (B, hk, cap), f"{name} must have shape {(B, hk, cap)}")
-    _cuda_tensor(lens, "lens", torch.int32, B)
-    _cuda_tensor(lens_out, "lens_out", torch.int32, B)
-    _cuda_tensor(kept, "kept", torch.int32, B * hk * max(0, int(budget)))
-    _check(lib.lva_evict_cache(_ptr(k_cache), _ptr(v_cache), _ptr(weight), _ptr(lens), _ptr(k_out), _ptr(v_out),
-                               _ptr(weight_out), _ptr(lens_out), _ptr(kept), B, hk, cap, d, int(budget), int(sinks),
-                               int(recent), ctypes.c_void_p(_stream(k_cache.device))))
+    cur = _device_of(k_cache, "k_cache")
+    if k_cache.dim() != 4:
+        _refuse("the caches must be [B, heads, capacity, d]")
+    shape = k_cache.shape
+    B, hk, cap, d = shape
+    wshape = (B, hk, cap)
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    _check(lib.lva_evict_cache(
+        _whole(k_cache, "k_cache", bf16, shape, cur), _whole(v_cache, "v_cache", bf16, shape, cur),
+        _whole(weight, "weight", f32, wshape, cur), _whole(lens, "lens", i32, (B,), cur),
+        _whole(k_out, "k_out", bf16, shape, cur), _whole(v_out, "v_out", bf16, shape, cur),
+        _whole(weight_out, "weight_out", f32, wshape, cur), _whole(lens_out, "lens_out", i32, (B,), cur),
+        _whole(kept, "kept", i32, (B, hk, budget), cur), B, hk, cap, d, budget, sinks, recent, _raw_stream(cur)))
     return k_out, v_out, weight_out, lens_out, kept
 
 

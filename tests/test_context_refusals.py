@@ -169,8 +169,19 @@ def test_cache_host_tensors_are_refused():
         lva.lva_evict_cache(c, c, w, i, c, c, w, i, torch.zeros((1, 1, 4), dtype=torch.int32), 4)
 
 
+class _Cuda:
+    """A host tensor that says it is on cuda:0 (for checks that read no data)."""
+    is_cuda = True
+
+    def __init__(self, t):
+        self.dtype, self.shape, self.stride = t.dtype, t.shape, t.stride
+
+    def get_device(self):
+        return 0
+
+
 def test_steps_view_wants_one_token_stride():
     from block_sparse_attention_lva_b200._binding import _steps_view
     t = _bf(2, 6, 2, 64)[:, :3]
     with pytest.raises(ValueError, match="one stride"):
-        _steps_view(t, "q", (2, 3, 2, 64))
+        _steps_view(_Cuda(t), "q", (2, 3, 2, 64), 0)
