@@ -24,6 +24,13 @@
 // each part stores its normalised O and its LSE (log2 units) in float32, joined later with
 // the parts of the sequences' own caches.
 //
+// Items: one CTA per SM starts per item until the SMs are full; a CTA that finishes loading an
+// item asks the hardware for one that has not started (cluster launch control) and goes on
+// with it, so the next item's loads and first Q K^T run under the current one's epilogue,
+// items are still handed out one by one in grid order, and nothing has to be counted in
+// memory.  The K producer decodes items and passes them to the other roles through a ring of
+// four in shared memory.
+//
 // Pipeline and warp roles are those of the block-sparse kernel (attn.cu): three S buffers in
 // TMEM next to O, P over its own S, Q K^T and P V issued by two threads, K and V rings of
 // three 128-row TMA tiles, eight softmax warps with half a row per thread, exponentials
@@ -71,30 +78,6 @@ struct PackedParams {
   int* err;
 };
 
-template <int D>
-struct Cfg {
-  static constexpr int KST = 3, VST = 3, NSB = 3;
-  static constexpr int Q_BYTES = BM * D * 2;
-  static constexpr int KV_BYTES = BN * D * 2;
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + Q_BYTES;
-  static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
-  static constexpr int OFF_BAR = OFF_V + VST * KV_BYTES;
-  // q_full, k_full/k_empty, v_full/v_empty, s_full, p_full, o_done, the two final drains and
-  // v_tail (the TMA of a V tile whose last rows are zeroed before v_full)
-  static constexpr int B_Q = 0, B_KF = 1, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST,
-                       B_SF = B_VE + VST, B_P = B_SF + NSB, B_O = B_P + NSB, B_FIN = B_O + NSB,
-                       B_FIN_PV = B_FIN + 1, B_VT = B_FIN_PV + 1, NUM_BARS = B_VT + 1;
-  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
-  static constexpr int SMEM_RAW = OFF_MISC + 16;
-  // at least 120 KB: one CTA, and one 512-column TMEM allocation, per SM
-  static constexpr int SMEM_BYTES = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;
-  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-  static constexpr uint32_t TM_S = 0, TM_O = 384;
-  static constexpr uint32_t IDESC_QK = idesc_bf16_f32(BM, BN, 0, 0);
-  static constexpr uint32_t IDESC_PV = idesc_bf16_f32(BM, D, 0, 1);
-};
-
 // A work item: rows [tok0, tok0 + rows / group) of the query tokens, key blocks [j0, j1) of
 // the key rows that start at k_row.
 struct Item {
@@ -105,7 +88,38 @@ struct Item {
   int64_t lim0;            // limit of the tile's first token before clamping to [0, lk]
   int causal;
   int j0, j_full, j1;      // blocks [j0, j_full) are seen in full by every row of the tile
-  bool live;               // false: nothing to do
+  int live;                // 0: nothing to do (in the ring: no more items)
+};
+
+constexpr int kItemRing = 4;
+constexpr int kItemReaders = kSoftmaxWarps + 3;   // every warp but the K producer
+
+template <int D>
+struct Cfg {
+  static constexpr int KST = 3, VST = 3, NSB = 3;
+  static constexpr int Q_BYTES = BM * D * 2;
+  static constexpr int KV_BYTES = BN * D * 2;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + Q_BYTES;
+  static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
+  static constexpr int OFF_BAR = OFF_V + VST * KV_BYTES;
+  // q_full, k_full/k_empty, v_full/v_empty, s_full, p_full, o_done, the two final drains,
+  // v_tail (the TMA of a V tile whose last rows are zeroed before v_full), q_empty (an item's
+  // Q K^T done), o_free (its O read), clc (the next item's answer), item_full/item_empty
+  static constexpr int B_Q = 0, B_KF = 1, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST,
+                       B_SF = B_VE + VST, B_P = B_SF + NSB, B_O = B_P + NSB, B_FIN = B_O + NSB,
+                       B_FIN_PV = B_FIN + 1, B_VT = B_FIN_PV + 1, B_QE = B_VT + 1, B_OF = B_QE + 1,
+                       B_CLC = B_OF + 1, B_IF = B_CLC + 1, B_IE = B_IF + kItemRing, NUM_BARS = B_IE + kItemRing;
+  static constexpr int OFF_MISC = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;
+  static constexpr int OFF_CLC = OFF_MISC + 16;
+  static constexpr int OFF_ITEMS = OFF_CLC + 16;
+  static constexpr int SMEM_RAW = OFF_ITEMS + kItemRing * int(sizeof(Item));
+  // at least 120 KB: one CTA, and one 512-column TMEM allocation, per SM
+  static constexpr int SMEM_BYTES = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  static constexpr uint32_t TM_S = 0, TM_O = 384;
+  static constexpr uint32_t IDESC_QK = idesc_bf16_f32(BM, BN, 0, 0);
+  static constexpr uint32_t IDESC_PV = idesc_bf16_f32(BM, D, 0, 1);
 };
 
 // Largest s with start(s) <= slot, start(s) = cu[s] / tok + s, found by the whole warp, 32
@@ -131,7 +145,7 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int n, int tok, 
 
 __device__ __forceinline__ Item item_at(const PackedParams& p, int64_t bid) {
   Item w;
-  w.live = false;
+  w.live = 0;
   w.split = 0;
   w.kvh = int(bid % p.kv_heads);
   const int64_t rest = bid / p.kv_heads;
@@ -150,7 +164,7 @@ __device__ __forceinline__ Item item_at(const PackedParams& p, int64_t bid) {
     const int full = int(p.total_k / BN);
     w.j_full = w.j1 < full ? w.j1 : full;
     if (w.j_full < w.j0) w.j_full = w.j0;
-    w.live = w.tok0 < w.q_end;
+    w.live = w.tok0 < w.q_end ? 1 : 0;
     return w;
   }
   // Packed: the last tiles of the last sequence first (a causal tile's work grows with its
@@ -181,7 +195,7 @@ __device__ __forceinline__ Item item_at(const PackedParams& p, int64_t bid) {
   w.j0 = 0;
   w.j1 = int((lim_last + BN - 1) / BN);
   w.j_full = int(lim_first / BN);
-  w.live = true;
+  w.live = 1;
   return w;
 }
 
@@ -220,10 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
         report_fault(p.err, 1, s);
     }
   }
-  const Item w = item_at(p, blockIdx.x);
-  if (!w.live) return;                            // the whole CTA: same item in every warp
-  const int n = w.j1 - w.j0;
-
   const uint32_t sQ = s_base + C::OFF_Q, sK = s_base + C::OFF_K, sV = s_base + C::OFF_V;
   const uint32_t bar0 = s_base + C::OFF_BAR;
   const uint32_t bar_q = bar0 + 8u * C::B_Q;
@@ -237,6 +247,12 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
   const uint32_t bar_final = bar0 + 8u * C::B_FIN;
   const uint32_t bar_final_pv = bar0 + 8u * C::B_FIN_PV;
   const uint32_t bar_v_tail = bar0 + 8u * C::B_VT;
+  const uint32_t bar_q_empty = bar0 + 8u * C::B_QE;
+  const uint32_t bar_o_free = bar0 + 8u * C::B_OF;
+  const uint32_t bar_clc = bar0 + 8u * C::B_CLC;
+  auto bar_item_full = [&](int s) { return bar0 + 8u * (C::B_IF + s); };
+  auto bar_item_empty = [&](int s) { return bar0 + 8u * (C::B_IE + s); };
+  Item* ring = reinterpret_cast<Item*>(smem + C::OFF_ITEMS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   volatile int* never = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);  // stays zero
@@ -254,6 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     mbar_init(bar_final, 1);
     mbar_init(bar_final_pv, 1);
     mbar_init(bar_v_tail, 1);
+    mbar_init(bar_q_empty, 1);
+    mbar_init(bar_o_free, kSoftmaxWarps);
+    mbar_init(bar_clc, 1);
+    for (int s = 0; s < kItemRing; ++s) { mbar_init(bar_item_full(s), 1); mbar_init(bar_item_empty(s), kItemReaders); }
     *abort_flag = 0;
     *never = 0;
     mbar_fence_init();
@@ -264,44 +284,109 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // The next item of a role warp (every warp but the K producer): 1, or 0 after the last one,
+  // or -1 when the wait gave up.  Pipeline positions T count key blocks over all items of this
+  // CTA, so ring slots, S buffers and their phases continue from one item to the next.
+  uint32_t ni = 0;
+  auto next_item = [&](Item& w) -> int {
+    const int s = int(ni % kItemRing);
+    if (!__all_sync(0xffffffffu, mbar_wait_sleep(bar_item_full(s), (ni / kItemRing) & 1, abort_flag))) return -1;
+    w = ring[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_item_empty(s));
+    ++ni;
+    return w.live;
+  };
+
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer: Q, K
-    if (lane == 0 && n > 0) {
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      mbar_arrive_expect_tx(bar_q, uint32_t(p.group * p.tok * D * 2));
-      for (int c = 0; c < D / 64; ++c)
-        tma_load_3d(sQ + c * BM * 128, &tm_q, c * 64, w.kvh * p.group, int32_t(w.tok0), bar_q);
-      int t = 0;
-      for (; t < n; ++t) {
-        const int s = t % C::KST;
-        if (t >= C::KST && !mbar_wait_sleep(bar_k_empty(s), ((t / C::KST) - 1) & 1, abort_flag)) {
-          *abort_flag = 1; report_fault(p.err, 5, 21); break;
+    // ------------------------------------------------------------ items; TMA producer: Q, K
+    if (lane == 0) { tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); }
+    const uint32_t resp = s_base + C::OFF_CLC;
+    uint32_t T = 0, answers = 0;
+    int nq = 0;
+    bool ok = true;
+    int64_t bid = blockIdx.x;
+    Item w;
+    while (ok) {
+      if (bid >= 0) w = item_at(p, bid);
+      else w.live = 0;
+      const int n = w.j1 - w.j0;
+      if (w.live || bid < 0) {
+        if (lane == 0) {
+          const int s = int(ni % kItemRing);
+          ok = ni < kItemRing || mbar_wait_sleep(bar_item_empty(s), ((ni / kItemRing) - 1) & 1, abort_flag);
+          if (ok) {
+            ring[s] = w;
+            mbar_arrive(bar_item_full(s));
+          }
         }
-        mbar_arrive_expect_tx(bar_k_full(s), C::KV_BYTES);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(sK + s * C::KV_BYTES + c * BN * 128, &tm_k, c * 64, w.kvh,
-                      int32_t(w.k_row + int64_t(w.j0 + t) * BN), bar_k_full(s));
+        ++ni;
       }
-      if (*abort_flag) {
-        for (int u = t > C::KST ? t - C::KST : 0; u < t; ++u)
-          mbar_wait(bar_k_full(u % C::KST), (u / C::KST) & 1, never);
-        mbar_wait(bar_q, 0, never);
+      if (bid < 0) { ok = __shfl_sync(0xffffffffu, ok, 0); break; }
+      if (lane == 0 && ok && w.live && n > 0) {
+        // Q is single-buffered: the previous item's Q K^T must have completed.
+        ok = nq == 0 || mbar_wait_sleep(bar_q_empty, (nq - 1) & 1, abort_flag);
+        if (ok) {
+          mbar_arrive_expect_tx(bar_q, uint32_t(p.group * p.tok * D * 2));
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sQ + c * BM * 128, &tm_q, c * 64, w.kvh * p.group, int32_t(w.tok0), bar_q);
+          ++nq;
+        }
+        for (int t = 0; ok && t < n; ++t) {
+          const int s = int(T % C::KST);
+          if (T >= uint32_t(C::KST) && !mbar_wait_sleep(bar_k_empty(s), int((T / C::KST) - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar_k_full(s), C::KV_BYTES);
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(sK + s * C::KV_BYTES + c * BN * 128, &tm_k, c * 64, w.kvh,
+                        int32_t(w.k_row + int64_t(w.j0 + t) * BN), bar_k_full(s));
+          ++T;
+        }
+      }
+      // The next item, asked for only now, three blocks before this one's end: asked for at its
+      // start, a CTA with a long item would hold on to one that others are free to take (a
+      // batch of short and long sequences took 97 us instead of 78).
+      int64_t next = -1;
+      if (lane == 0 && ok) {
+        mbar_arrive_expect_tx(bar_clc, 16);
+        clc_try_cancel(resp, bar_clc);
+        if (mbar_wait_sleep(bar_clc, answers & 1, never)) {
+          next = clc_answer(resp);
+          fence_proxy_async_smem();              // read before the next answer is written
+        } else {
+          ok = false;
+        }
+      }
+      ++answers;
+      bid = __shfl_sync(0xffffffffu, next, 0);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {
+      if (!ok) { *abort_flag = 1; report_fault(p.err, 5, 21); }
+      if (*abort_flag) {                           // every load in flight lands before the CTA ends
+        for (uint32_t u = T > uint32_t(C::KST) ? T - C::KST : 0; u < T; ++u)
+          mbar_wait(bar_k_full(int(u % C::KST)), int(u / C::KST) & 1, never);
+        if (nq > 0) mbar_wait(bar_q, (nq - 1) & 1, never);
       }
     }
   } else if (warp == kVWarp) {
     // ------------------------------------------------------------ TMA producer: V
-    if (n > 0) {
-      if (lane == 0) tma_prefetch_desc(&tm_v);
+    if (lane == 0) tma_prefetch_desc(&tm_v);
+    uint32_t T = 0, tails = 0;
+    int got = 1;
+    Item w;
+    while ((got = next_item(w)) == 1) {
+      const int n = w.j1 - w.j0;
       bool ok = true;
-      int t = 0;
-      for (; t < n; ++t) {
-        const int s = t % C::VST;
+      for (int t = 0; ok && t < n; ++t) {
+        const int s = int(T % C::VST);
         const int64_t left = w.lk - int64_t(w.j0 + t) * BN;      // keys of the sequence from here on
-        const bool tail = left < BN;                             // at most the last block
+        const bool tail = left < BN;                             // at most an item's last block
         if (lane == 0) {
-          if (t >= C::VST && !mbar_wait_sleep(bar_v_empty(s), ((t / C::VST) - 1) & 1, abort_flag)) {
-            *abort_flag = 1; report_fault(p.err, 5, 22); ok = false;
+          if (T >= uint32_t(C::VST) && !mbar_wait_sleep(bar_v_empty(s), int((T / C::VST) - 1) & 1, abort_flag)) {
+            ok = false;
           } else {
             const uint32_t bar = tail ? bar_v_tail : bar_v_full(s);
             mbar_arrive_expect_tx(bar, C::KV_BYTES);
@@ -312,82 +397,109 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
+        ++T;
         if (tail) {
           // Rows past the sequence's end hold other sequences' values, or anything: zeroed,
           // because their weight of zero times NaN or infinity would not be zero.
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_v_tail, 0, never));
-          if (ok) {
-            for (int c = 0; c < D / 64; ++c) {
-              uint8_t* rows = smem + C::OFF_V + s * C::KV_BYTES + c * BN * 128;
-              for (int x = int(left) * 8 + lane; x < BN * 8; x += 32)
-                reinterpret_cast<uint4*>(rows)[x] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_v_full(s));
-          } else if (lane == 0) {
-            *abort_flag = 1; report_fault(p.err, 5, 23);
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_v_tail, tails & 1, never));
+          ++tails;
+          if (!ok) break;
+          for (int c = 0; c < D / 64; ++c) {
+            uint8_t* rows = smem + C::OFF_V + s * C::KV_BYTES + c * BN * 128;
+            for (int x = int(left) * 8 + lane; x < BN * 8; x += 32)
+              reinterpret_cast<uint4*>(rows)[x] = make_uint4(0u, 0u, 0u, 0u);
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_v_full(s));
         }
       }
-      if (lane == 0 && *abort_flag) {
-        for (int u = t > C::VST ? t - C::VST : 0; u < t; ++u)
-          mbar_wait(bar_v_full(u % C::VST), (u / C::VST) & 1, never);
-      }
+      if (!ok) { got = -1; break; }
+    }
+    if (got < 0 && lane == 0) {
+      *abort_flag = 1;
+      report_fault(p.err, 5, 22);
+      for (uint32_t u = T > uint32_t(C::VST) ? T - C::VST : 0; u < T; ++u)
+        mbar_wait(bar_v_full(int(u % C::VST)), int(u / C::VST) & 1, never);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer: S = Q K^T
-    if (lane == 0 && n > 0) {
-      const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024);
-      const uint64_t k_desc = smem_desc_sw128(sK, 16, 1024);
-      bool ok = mbar_wait_sleep(bar_q, 0, abort_flag);
-      bool any_mma = false;
-      for (int t = 0; ok && t < n; ++t) {
-        const int s = t % C::KST, b = t % C::NSB;
-        if (!mbar_wait_sleep(bar_k_full(s), (t / C::KST) & 1, abort_flag)) { ok = false; break; }
-        if (t >= C::NSB && !mbar_wait_sleep(bar_o_done(b), ((t / C::NSB) - 1) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint64_t ks = k_desc + uint64_t((s * C::KV_BYTES) >> 4);
-        const uint32_t s_tm = tmem + C::TM_S + 128 * b;
+    const uint64_t q_desc = smem_desc_sw128(sQ, 16, 1024);
+    const uint64_t k_desc = smem_desc_sw128(sK, 16, 1024);
+    uint32_t T = 0;
+    int nq = 0, got = 1;
+    Item w;
+    while ((got = next_item(w)) == 1) {
+      const int n = w.j1 - w.j0;
+      if (n == 0) continue;
+      bool ok = true;
+      if (lane == 0) {
+        ok = mbar_wait_sleep(bar_q, nq & 1, abort_flag);
+        for (int t = 0; ok && t < n; ++t, ++T) {
+          const int s = int(T % C::KST), b = int(T % C::NSB);
+          if (!mbar_wait_sleep(bar_k_full(s), int(T / C::KST) & 1, abort_flag)) { ok = false; break; }
+          // S_b is free again once the P that went over it has been multiplied
+          if (T >= uint32_t(C::NSB) && !mbar_wait_sleep(bar_o_done(b), int((T / C::NSB) - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ks = k_desc + uint64_t((s * C::KV_BYTES) >> 4);
+          const uint32_t s_tm = tmem + C::TM_S + 128 * b;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_f16_ss(s_tm, q_desc + uint64_t(((kk / 4) * BM * 128 + (kk % 4) * 32) >> 4),
-                      ks + uint64_t(((kk / 4) * BN * 128 + (kk % 4) * 32) >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
-        umma_commit(bar_s_full(b));
-        umma_commit(bar_k_empty(s));
-        any_mma = true;
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_f16_ss(s_tm, q_desc + uint64_t(((kk / 4) * BM * 128 + (kk % 4) * 32) >> 4),
+                        ks + uint64_t(((kk / 4) * BN * 128 + (kk % 4) * 32) >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
+          umma_commit(bar_s_full(b));
+          umma_commit(bar_k_empty(s));
+        }
+        if (ok) umma_commit(bar_q_empty);          // Q may be replaced
       }
-      if (!ok) { *abort_flag = 1; report_fault(p.err, 5, 24); }
-      if (any_mma) {
-        umma_commit(bar_final);
-        mbar_wait(bar_final, 0, never);
-      }
+      ++nq;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) { got = -1; break; }
+    }
+    if (lane == 0) {
+      if (got < 0) { *abort_flag = 1; report_fault(p.err, 5, 24); }
+      umma_commit(bar_final);                      // every MMA of this thread before TMEM is released
+      mbar_wait(bar_final, 0, never);
     }
   } else if (warp == kPVWarp) {
     // ------------------------------------------------------------ MMA issuer: O += P V
-    if (lane == 0 && n > 0) {
-      const uint64_t v_desc = smem_desc_sw128(sV, BN * 128, 1024);
-      bool ok = true, any_mma = false;
-      for (int t = 0; ok && t < n; ++t) {
-        const int s = t % C::VST, b = t % C::NSB;
-        if (!mbar_wait_sleep(bar_p_full(b), (t / C::NSB) & 1, abort_flag)) { ok = false; break; }
-        if (!mbar_wait_sleep(bar_v_full(s), (t / C::VST) & 1, abort_flag)) { ok = false; break; }
-        tc_fence_after();
-        const uint64_t vs = v_desc + uint64_t((s * C::KV_BYTES) >> 4);
-        const uint32_t p_tm = tmem + C::TM_S + 128 * b;
+    const uint64_t v_desc = smem_desc_sw128(sV, BN * 128, 1024);
+    uint32_t T = 0;
+    int nq = 0, got = 1;
+    Item w;
+    while ((got = next_item(w)) == 1) {
+      const int n = w.j1 - w.j0;
+      if (n == 0) continue;
+      bool ok = true;
+      if (lane == 0) {
+        // an item's first P V overwrites O: the previous item's must have been read
+        if (nq > 0) ok = mbar_wait_sleep(bar_o_free, (nq - 1) & 1, abort_flag);
+        for (int t = 0; ok && t < n; ++t, ++T) {
+          const int s = int(T % C::VST), b = int(T % C::NSB);
+          if (!mbar_wait_sleep(bar_p_full(b), int(T / C::NSB) & 1, abort_flag)) { ok = false; break; }
+          if (!mbar_wait_sleep(bar_v_full(s), int(T / C::VST) & 1, abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t vs = v_desc + uint64_t((s * C::KV_BYTES) >> 4);
+          const uint32_t p_tm = tmem + C::TM_S + 128 * b;
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          umma_f16_ts(tmem + C::TM_O, p_tm + kk * 8, vs + uint64_t((kk * 16 * 128) >> 4), C::IDESC_PV,
-                      (t > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(bar_v_empty(s));
-        umma_commit(bar_o_done(b));
-        any_mma = true;
+          for (int kk = 0; kk < BN / 16; ++kk)
+            umma_f16_ts(tmem + C::TM_O, p_tm + kk * 8, vs + uint64_t((kk * 16 * 128) >> 4), C::IDESC_PV,
+                        (t > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(bar_v_empty(s));
+          umma_commit(bar_o_done(b));
+        }
       }
-      if (!ok) { *abort_flag = 1; report_fault(p.err, 5, 25); }
-      if (any_mma) {
-        umma_commit(bar_final_pv);
-        mbar_wait(bar_final_pv, 0, never);
-      }
+      ++nq;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) { got = -1; break; }
+    }
+    if (lane == 0) {
+      if (got < 0) { *abort_flag = 1; report_fault(p.err, 5, 25); }
+      umma_commit(bar_final_pv);
+      mbar_wait(bar_final_pv, 0, never);
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
@@ -398,9 +510,15 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     const int row = quarter * 32 + sel * 16 + (lane & 15);
     const uint32_t lane_off = uint32_t(quarter * 32 + sel * 16) << 16;
     const float c = p.scale_log2;
-    const int tok_in = row / p.group;
+    const int tok_in = row / p.group, head_in = row - tok_in * p.group;
+    const bool row_used = row < p.tok * p.group;
+    uint32_t T = 0;
+    int got = 1;
+    Item w;
+    while ((got = next_item(w)) == 1) {
+    const int n = w.j1 - w.j0;
     const int64_t token = w.tok0 + tok_in;
-    const bool store = row < p.tok * p.group && token < w.q_end;
+    const bool store = row_used && token < w.q_end;
     // Keys this row sees, counted from the sequence's first key.
     int64_t limit = w.causal ? w.lim0 + tok_in : w.lim0;
     limit = limit > w.lk ? w.lk : limit;
@@ -413,8 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     // (the MUFU's 2^-inf; the polynomial would give 2^-125).
     auto step = [&](int t, auto masked_tag) -> bool {
       constexpr bool MASKED = decltype(masked_tag)::value;
-      const int b = t % C::NSB;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full(b), (t / C::NSB) & 1, abort_flag))) return false;
+      const int b = int(T % C::NSB);
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full(b), int(T / C::NSB) & 1, abort_flag))) return false;
       tc_fence_after();
       uint32_t sr[HALF];
 #pragma unroll
@@ -467,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
       f2_unpack(acc[1], b0, b1);
       l = l * alpha + ((a0 + a1) + (b0 + b1));
       if (t >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_o_done((t - 1) % C::NSB), ((t - 1) / C::NSB) & 1, abort_flag)))
+        if (!__all_sync(0xffffffffu, mbar_wait(bar_o_done(int((T - 1) % C::NSB)), int((T - 1) / C::NSB) & 1, abort_flag)))
           return false;
         tc_fence_after();
         rescale_o<DH>(tmem + lane_off + C::TM_O, alpha);
@@ -482,9 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     // A block that every row sees, after the first: exponentials against the current
     // reference while the block max is found alongside; given up (2) before anything is
     // stored when a row's max outgrows its reference by 2^8.
-    auto step_spec = [&](int t) -> int {
-      const int b = t % C::NSB;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full(b), (t / C::NSB) & 1, abort_flag))) return 0;
+    auto step_spec = [&]() -> int {
+      const int b = int(T % C::NSB);
+      if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full(b), int(T / C::NSB) & 1, abort_flag))) return 0;
       tc_fence_after();
       uint32_t sr[HALF];
 #pragma unroll
@@ -530,76 +648,83 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
 
     const int t_full = w.j_full - w.j0;
     int t = 0;
-    if (!__any_sync(0xffffffffu, store)) {
+    const bool idle = !__any_sync(0xffffffffu, store);
+    if (idle) {
       // No row of this warp is stored (a tile of few rows): its P may hold anything.
-      for (; ok && t < n; ++t) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(t % C::NSB), (t / C::NSB) & 1, abort_flag));
-        if (ok && lane == 0) mbar_arrive(bar_p_full(t % C::NSB));
+      for (; ok && t < n; ++t, ++T) {
+        const int b = int(T % C::NSB);
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(b), int(T / C::NSB) & 1, abort_flag));
+        if (ok && lane == 0) mbar_arrive(bar_p_full(b));
       }
     }
-    for (; ok && t < t_full; ++t) {
+    for (; ok && t < t_full; ++t, ++T) {
       int r = 2;
-      if (t > 0) r = step_spec(t);
+      if (t > 0) r = step_spec();
       if (r == 0) ok = false;
       else if (r == 2) ok = step(t, std::false_type{});
     }
-    for (; ok && t < n; ++t) ok = step(t, std::true_type{});
+    for (; ok && t < n; ++t, ++T) ok = step(t, std::true_type{});
 
     // ---------------------------------------------------------- epilogue
     if (ok && n > 0) {
-      const int u = n - 1;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_o_done(u % C::NSB), (u / C::NSB) & 1, abort_flag));
+      const uint32_t u = T - 1;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_o_done(int(u % C::NSB)), int(u / C::NSB) & 1, abort_flag));
       tc_fence_after();
     }
-    if (ok) {
-      const float l_row = l + __shfl_xor_sync(0xffffffffu, l, 16);
-      const bool none = !sees || l_row == 0.f;     // a NaN sum goes through as NaN
-      const float inv_l = none ? 0.f : 1.f / l_row;
-      const int head = w.kvh * p.group + (row - tok_in * p.group);
-      const int64_t part_row = ((int64_t(w.split) * p.kv_heads + w.kvh) * p.total_q + token) * p.group +
-                               (row - tok_in * p.group);
-#pragma unroll 1
-      for (int q = 0; q < DH / 32; ++q) {
-        uint32_t ov[32] = {};
-        __syncwarp();                              // the load is the whole warp's
-        if (n > 0) {
-          tmem_ld_16x2_32<DH>(tmem + lane_off + C::TM_O + q * 32, ov);
-          tmem_wait_ld();
+    if (!ok) { got = -1; break; }
+    uint32_t ov[DH] = {};
+    if (n > 0) {
+#pragma unroll
+      for (int q = 0; q < DH / 32; ++q)
+        tmem_ld_16x2_32<DH>(tmem + lane_off + C::TM_O + q * 32, *reinterpret_cast<uint32_t(*)[32]>(ov + q * 32));
+      tmem_wait_ld();
+      // O is in registers: the next item's first P V may overwrite it.
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_o_free);
+    }
+    const float l_row = l + __shfl_xor_sync(0xffffffffu, l, 16);
+    const bool none = !sees || l_row == 0.f;       // a NaN sum goes through as NaN
+    const float inv_l = none ? 0.f : 1.f / l_row;
+    const int head = w.kvh * p.group + head_in;
+    const int64_t part_row = ((int64_t(w.split) * p.kv_heads + w.kvh) * p.total_q + token) * p.group + head_in;
+    if (store) {
+      if (p.splits > 0) {
+        float* dst = p.part_o + part_row * D + hf * DH;
+#pragma unroll
+        for (int e4 = 0; e4 < DH / 4; ++e4) {
+          float4 f;
+          f.x = none ? 0.f : __uint_as_float(ov[4 * e4]) * inv_l;
+          f.y = none ? 0.f : __uint_as_float(ov[4 * e4 + 1]) * inv_l;
+          f.z = none ? 0.f : __uint_as_float(ov[4 * e4 + 2]) * inv_l;
+          f.w = none ? 0.f : __uint_as_float(ov[4 * e4 + 3]) * inv_l;
+          reinterpret_cast<float4*>(dst)[e4] = f;
         }
-        if (!store) {
-        } else if (p.splits > 0) {
-          float* dst = p.part_o + part_row * D + hf * DH + q * 32;
+      } else {
+        __nv_bfloat16* dst = p.o + token * p.o_token + int64_t(head) * p.o_head + hf * DH;
+        uint32_t wv[DH / 2];
 #pragma unroll
-          for (int e4 = 0; e4 < 8; ++e4) {
-            float4 f;
-            f.x = none ? 0.f : __uint_as_float(ov[4 * e4]) * inv_l;
-            f.y = none ? 0.f : __uint_as_float(ov[4 * e4 + 1]) * inv_l;
-            f.z = none ? 0.f : __uint_as_float(ov[4 * e4 + 2]) * inv_l;
-            f.w = none ? 0.f : __uint_as_float(ov[4 * e4 + 3]) * inv_l;
-            reinterpret_cast<float4*>(dst)[e4] = f;
-          }
+        for (int e = 0; e < DH / 2; ++e)
+          wv[e] = none ? 0u : pack_bf16x2(__uint_as_float(ov[2 * e]) * inv_l, __uint_as_float(ov[2 * e + 1]) * inv_l);
+        if (p.o_align32) {
+#pragma unroll
+          for (int e8 = 0; e8 < DH / 16; ++e8)
+            st_global_v8(dst + e8 * 16, *reinterpret_cast<const uint32_t(*)[8]>(wv + e8 * 8));
         } else {
-          __nv_bfloat16* dst = p.o + token * p.o_token + int64_t(head) * p.o_head + hf * DH + q * 32;
-          uint32_t wv[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            wv[e] = none ? 0u : pack_bf16x2(__uint_as_float(ov[2 * e]) * inv_l, __uint_as_float(ov[2 * e + 1]) * inv_l);
-          if (p.o_align32) {
-            st_global_v8(dst, *reinterpret_cast<const uint32_t(*)[8]>(wv));
-            st_global_v8(dst + 16, *reinterpret_cast<const uint32_t(*)[8]>(wv + 8));
-          } else {
-#pragma unroll
-            for (int e4 = 0; e4 < 4; ++e4)
-              reinterpret_cast<uint4*>(dst)[e4] = make_uint4(wv[4 * e4], wv[4 * e4 + 1], wv[4 * e4 + 2], wv[4 * e4 + 3]);
-          }
+          for (int e4 = 0; e4 < DH / 8; ++e4)
+            reinterpret_cast<uint4*>(dst)[e4] = make_uint4(wv[4 * e4], wv[4 * e4 + 1], wv[4 * e4 + 2], wv[4 * e4 + 3]);
         }
       }
-      if (store && hf == 0) {
+      if (hf == 0) {
         const float lse2 = none ? -INFINITY : m_ref + __log2f(l_row);
         if (p.splits > 0) p.part_lse[part_row] = lse2;
         else p.lse[int64_t(head) * p.total_q + token] = lse2 * kLn2;
       }
-    } else {
+    }
+    __syncwarp();                                  // the next item's loads are the whole warp's
+    }
+    if (got < 0) {
       *abort_flag = 1;
       if (lane == 0) report_fault(p.err, 5, 26);
     }
