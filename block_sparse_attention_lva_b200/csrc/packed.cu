@@ -37,7 +37,6 @@
 // against the current reference while the block's maximum is found alongside, O rescaled
 // only when a row's maximum grows by more than 2^8.
 #include <cstdint>
-#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -71,7 +70,7 @@ struct PackedParams {
   float scale_log2;                // scale * log2(e)
   __nv_bfloat16* o;
   float* lse;                      // [Hq, total_q]
-  int o_align32;
+  int o_boxes;                     // 16 rows are whole tokens: O has a map with boxes of them
   int splits;                      // 0: packed; > 0: parts of the shared prefix
   float* part_o;                   // [splits, kv_heads, total_q, group, D]
   float* part_lse;                 // [splits, kv_heads, total_q, group], log2 units
@@ -83,32 +82,40 @@ struct PackedParams {
 struct Item {
   int kvh;
   int split;
-  int64_t tok0, q_end;     // first query token of the tile, end of its sequence
-  int64_t k_row, lk;       // first key row of the sequence, its keys
-  int64_t lim0;            // limit of the tile's first token before clamping to [0, lk]
+  int tok0, q_end;         // first query token of the tile, end of its sequence
+  int k_row, lk;           // first key row of the sequence, its keys
+  int lim0;                // limit of the tile's first token, possibly below zero
   int causal;
   int j0, j_full, j1;      // blocks [j0, j_full) are seen in full by every row of the tile
   int live;                // 0: nothing to do (in the ring: no more items)
+  // The key block at step t: the masked ones first, so that an item has one step that must
+  // find its maximum before its exponentials (the first) instead of two.
+  __device__ __forceinline__ int block(int t) const {
+    const int masked = j1 - j_full;
+    return t < masked ? j_full + t : j0 + t - masked;
+  }
 };
 
 constexpr int kItemRing = 4;
+constexpr int kAhead = 6;
 constexpr int kItemReaders = kSoftmaxWarps + 3;   // every warp but the K producer
 
 template <int D>
 struct Cfg {
-  static constexpr int KST = 3, VST = 3, NSB = 3;
+  static constexpr int KST = 3, VST = D == 128 ? 2 : 3, NSB = 3;
+  static constexpr int QST = 2;                    // the next item's Q loads during the current one
   static constexpr int Q_BYTES = BM * D * 2;
   static constexpr int KV_BYTES = BN * D * 2;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + Q_BYTES;
+  static constexpr int OFF_K = OFF_Q + QST * Q_BYTES;
   static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
   static constexpr int OFF_BAR = OFF_V + VST * KV_BYTES;
   // q_full, k_full/k_empty, v_full/v_empty, s_full, p_full, o_done, the two final drains,
   // v_tail (the TMA of a V tile whose last rows are zeroed before v_full), q_empty (an item's
-  // Q K^T done), o_free (its O read), clc (the next item's answer), item_full/item_empty
-  static constexpr int B_Q = 0, B_KF = 1, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST,
+  // Q K^T done and its O stored), o_free (its O read), clc (the next item's answer), item_full/item_empty
+  static constexpr int B_Q = 0, B_KF = B_Q + QST, B_KE = B_KF + KST, B_VF = B_KE + KST, B_VE = B_VF + VST,
                        B_SF = B_VE + VST, B_P = B_SF + NSB, B_O = B_P + NSB, B_FIN = B_O + NSB,
-                       B_FIN_PV = B_FIN + 1, B_VT = B_FIN_PV + 1, B_QE = B_VT + 1, B_OF = B_QE + 1,
+                       B_FIN_PV = B_FIN + 1, B_VT = B_FIN_PV + 1, B_QE = B_VT + 1, B_OF = B_QE + QST,
                        B_CLC = B_OF + 1, B_IF = B_CLC + 1, B_IE = B_IF + kItemRing, NUM_BARS = B_IE + kItemRing;
   static constexpr int OFF_MISC = (OFF_BAR + NUM_BARS * 8 + 15) / 16 * 16;
   static constexpr int OFF_CLC = OFF_MISC + 16;
@@ -126,14 +133,17 @@ struct Cfg {
 // probes a round; -1 when there is none.  start is strictly increasing for a valid cu, and
 // sequence s needs at most start(s + 1) - start(s) tiles; whatever cu holds, the answer stays
 // in [-1, n).
-__device__ __forceinline__ int find_sequence(const int32_t* cu, int n, int tok, int64_t slot) {
+__device__ __forceinline__ int find_sequence(const int32_t* cu, int n, int tok, uint32_t slot) {
   const int lane = threadIdx.x & 31;
   int lo = 0, cnt = n;
   for (;;) {
     const int step = (cnt + 31) / 32;
     const int idx = lo + lane * step;
     bool le = false;
-    if (lane * step < cnt) le = int64_t(__ldg(cu + idx) / tok) + idx <= slot;
+    if (lane * int64_t(step) < cnt) {
+      const int32_t c = __ldg(cu + idx);
+      le = c < 0 || uint32_t(c) / uint32_t(tok) + uint32_t(idx) <= slot;
+    }
     const int k = __popc(__ballot_sync(0xffffffffu, le));
     if (k == 0) return lo == 0 ? -1 : lo;
     const int end = lo + cnt;
@@ -143,24 +153,26 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int n, int tok, 
   }
 }
 
-__device__ __forceinline__ Item item_at(const PackedParams& p, int64_t bid) {
+// All item arithmetic is in 32 bits: tokens, tiles and the grid stay below 2^31.
+__device__ __forceinline__ Item item_at(const PackedParams& p, uint32_t bid) {
   Item w;
   w.live = 0;
   w.split = 0;
-  w.kvh = int(bid % p.kv_heads);
-  const int64_t rest = bid / p.kv_heads;
+  const uint32_t rest = bid / uint32_t(p.kv_heads);
+  w.kvh = int(bid - rest * p.kv_heads);
   if (p.splits > 0) {
     // Shared prefix: parts fastest after the head, so that the parts of a tile run together.
-    w.split = int(rest % p.splits);
-    w.tok0 = (rest / p.splits) * p.tok;
-    w.q_end = p.total_q;
+    const uint32_t tile = rest / uint32_t(p.splits);
+    w.split = int(rest - tile * p.splits);
+    w.tok0 = int(tile * p.tok);
+    w.q_end = int(p.total_q);
     w.k_row = 0;
-    w.lk = p.total_k;
-    w.lim0 = p.total_k;
+    w.lk = int(p.total_k);
+    w.lim0 = int(p.total_k);
     w.causal = 0;
-    const int64_t nblk = (p.total_k + BN - 1) / BN;
-    w.j0 = int(nblk * w.split / p.splits);
-    w.j1 = int(nblk * (w.split + 1) / p.splits);
+    const uint32_t nblk = uint32_t(p.total_k + BN - 1) / BN;     // parts <= 32, blocks < 2^25
+    w.j0 = int(nblk * w.split / uint32_t(p.splits));
+    w.j1 = int(nblk * (w.split + 1) / uint32_t(p.splits));
     const int full = int(p.total_k / BN);
     w.j_full = w.j1 < full ? w.j1 : full;
     if (w.j_full < w.j0) w.j_full = w.j0;
@@ -169,32 +181,31 @@ __device__ __forceinline__ Item item_at(const PackedParams& p, int64_t bid) {
   }
   // Packed: the last tiles of the last sequence first (a causal tile's work grows with its
   // place, so the shortest tiles fill the tail), the heads of a tile next to one another.
-  const int64_t slots = p.total_q / p.tok + p.num_seqs;
-  const int64_t slot = slots - 1 - rest;
+  const uint32_t slot = uint32_t(p.total_q) / uint32_t(p.tok) + uint32_t(p.num_seqs) - 1u - rest;
   const int s = find_sequence(p.cu_q, p.num_seqs, p.tok, slot);
   if (s < 0) return w;
-  const int64_t a = __ldg(p.cu_q + s), b = __ldg(p.cu_q + s + 1);
-  const int64_t ka = __ldg(p.cu_k + s), kb = __ldg(p.cu_k + s + 1);
+  const int a = __ldg(p.cu_q + s), b = __ldg(p.cu_q + s + 1);
+  const int ka = __ldg(p.cu_k + s), kb = __ldg(p.cu_k + s + 1);
   if (!(a >= 0 && a <= b && b <= p.total_q && ka >= 0 && ka <= kb && kb <= p.total_k)) return w;
-  const int64_t tile = slot - (a / p.tok + s);
-  const int64_t i0 = tile * p.tok;                       // first token of the tile in its sequence
-  if (tile < 0 || i0 >= b - a) return w;
-  const int64_t lq = b - a, lk = kb - ka;
-  const int64_t last = (i0 + p.tok < lq ? i0 + p.tok : lq) - 1;
+  const uint32_t first_slot = uint32_t(a) / uint32_t(p.tok) + uint32_t(s);
+  const int lq = b - a, lk = kb - ka;
+  // first token of the tile in its sequence; slots before the sequence's or past its tiles
+  const int64_t i0_wide = (int64_t(slot) - int64_t(first_slot)) * p.tok;
+  if (i0_wide < 0 || i0_wide >= lq) return w;
+  const int i0 = int(i0_wide);
+  const int last = (i0 + p.tok < lq ? i0 + p.tok : lq) - 1;
   w.tok0 = a + i0;
   w.q_end = b;
   w.k_row = ka;
   w.lk = lk;
   w.causal = p.causal;
-  w.lim0 = p.causal ? i0 + lk - lq + 1 : lk;
-  int64_t lim_last = p.causal ? last + lk - lq + 1 : lk;
-  if (lim_last > lk) lim_last = lk;
-  if (lim_last < 0) lim_last = 0;
-  int64_t lim_first = w.lim0 > lk ? lk : w.lim0;
-  if (lim_first < 0) lim_first = 0;
+  w.lim0 = p.causal ? i0 + 1 + (lk - lq) : lk;
+  int lim_last = p.causal ? last + 1 + (lk - lq) : lk;
+  lim_last = lim_last < 0 ? 0 : lim_last;          // at most lk: last < lq
+  const int lim_first = w.lim0 < 0 ? 0 : w.lim0;
   w.j0 = 0;
-  w.j1 = int((lim_last + BN - 1) / BN);
-  w.j_full = int(lim_first / BN);
+  w.j1 = int((uint32_t(lim_last) + BN - 1) / BN);
+  w.j_full = lim_first / BN;
   w.live = 1;
   return w;
 }
@@ -216,7 +227,7 @@ __device__ __noinline__ void rescale_o(uint32_t taddr, float alpha) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-    const __grid_constant__ CUtensorMap tm_v, const PackedParams p) {
+    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const PackedParams p) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t s_base = smem_u32(smem);
@@ -236,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
   }
   const uint32_t sQ = s_base + C::OFF_Q, sK = s_base + C::OFF_K, sV = s_base + C::OFF_V;
   const uint32_t bar0 = s_base + C::OFF_BAR;
-  const uint32_t bar_q = bar0 + 8u * C::B_Q;
+  auto bar_q = [&](int s) { return bar0 + 8u * (C::B_Q + s); };
   auto bar_k_full = [&](int s) { return bar0 + 8u * (C::B_KF + s); };
   auto bar_k_empty = [&](int s) { return bar0 + 8u * (C::B_KE + s); };
   auto bar_v_full = [&](int s) { return bar0 + 8u * (C::B_VF + s); };
@@ -247,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
   const uint32_t bar_final = bar0 + 8u * C::B_FIN;
   const uint32_t bar_final_pv = bar0 + 8u * C::B_FIN_PV;
   const uint32_t bar_v_tail = bar0 + 8u * C::B_VT;
-  const uint32_t bar_q_empty = bar0 + 8u * C::B_QE;
+  auto bar_q_empty = [&](int s) { return bar0 + 8u * (C::B_QE + s); };
   const uint32_t bar_o_free = bar0 + 8u * C::B_OF;
   const uint32_t bar_clc = bar0 + 8u * C::B_CLC;
   auto bar_item_full = [&](int s) { return bar0 + 8u * (C::B_IF + s); };
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(bar_q, 1);
+    for (int s = 0; s < C::QST; ++s) { mbar_init(bar_q(s), 1); mbar_init(bar_q_empty(s), 1 + kSoftmaxWarps); }
     for (int s = 0; s < C::KST; ++s) { mbar_init(bar_k_full(s), 1); mbar_init(bar_k_empty(s), 1); }
     for (int s = 0; s < C::VST; ++s) { mbar_init(bar_v_full(s), 1); mbar_init(bar_v_empty(s), 1); }
     for (int b = 0; b < C::NSB; ++b) {
@@ -270,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     mbar_init(bar_final, 1);
     mbar_init(bar_final_pv, 1);
     mbar_init(bar_v_tail, 1);
-    mbar_init(bar_q_empty, 1);
     mbar_init(bar_o_free, kSoftmaxWarps);
     mbar_init(bar_clc, 1);
     for (int s = 0; s < kItemRing; ++s) { mbar_init(bar_item_full(s), 1); mbar_init(bar_item_empty(s), kItemReaders); }
@@ -305,12 +315,13 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     uint32_t T = 0, answers = 0;
     int nq = 0;
     bool ok = true;
-    int64_t bid = blockIdx.x;
+    int64_t bid = blockIdx.x;                      // -1: no more items
     Item w;
     while (ok) {
-      if (bid >= 0) w = item_at(p, bid);
+      if (bid >= 0) w = item_at(p, uint32_t(bid));
       else w.live = 0;
-      const int n = w.j1 - w.j0;
+      const int n = w.live ? w.j1 - w.j0 : 0;
+      int64_t next = -1;
       if (w.live || bid < 0) {
         if (lane == 0) {
           const int s = int(ni % kItemRing);
@@ -323,16 +334,29 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
         ++ni;
       }
       if (bid < 0) { ok = __shfl_sync(0xffffffffu, ok, 0); break; }
-      if (lane == 0 && ok && w.live && n > 0) {
-        // Q is single-buffered: the previous item's Q K^T must have completed.
-        ok = nq == 0 || mbar_wait_sleep(bar_q_empty, (nq - 1) & 1, abort_flag);
-        if (ok) {
-          mbar_arrive_expect_tx(bar_q, uint32_t(p.group * p.tok * D * 2));
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(sQ + c * BM * 128, &tm_q, c * 64, w.kvh * p.group, int32_t(w.tok0), bar_q);
-          ++nq;
-        }
-        for (int t = 0; ok && t < n; ++t) {
+      // The next item is asked for kAhead blocks before this one's end, which hides the answer's
+      // latency; asked for earlier, a CTA with a long item would hold on to one that others
+      // are free to take (a batch of short and long sequences took 97 us instead of 78).
+      if (lane == 0 && ok) {
+        const int t_ask = n > kAhead ? n - kAhead : 0;
+        auto ask = [&] {
+          mbar_arrive_expect_tx(bar_clc, 16);
+          clc_try_cancel(resp, bar_clc);
+        };
+        if (n == 0) ask();
+        bool asked = n == 0;
+        for (int t = 0; ok && t < n; ++t, ++T) {
+          if (t == t_ask) { ask(); asked = true; }
+          if (t == 0) {
+            // Q's buffer is free once the item before the previous one has been stored.
+            const int s = nq % C::QST;
+            ok = nq < C::QST || mbar_wait_sleep(bar_q_empty(s), ((nq / C::QST) - 1) & 1, abort_flag);
+            if (!ok) break;
+            mbar_arrive_expect_tx(bar_q(s), uint32_t(p.group * p.tok * D * 2));
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(sQ + s * C::Q_BYTES + c * BM * 128, &tm_q, c * 64, w.kvh * p.group, w.tok0, bar_q(s));
+            ++nq;
+          }
           const int s = int(T % C::KST);
           if (T >= uint32_t(C::KST) && !mbar_wait_sleep(bar_k_empty(s), int((T / C::KST) - 1) & 1, abort_flag)) {
             ok = false;
@@ -341,22 +365,16 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
           mbar_arrive_expect_tx(bar_k_full(s), C::KV_BYTES);
           for (int c = 0; c < D / 64; ++c)
             tma_load_3d(sK + s * C::KV_BYTES + c * BN * 128, &tm_k, c * 64, w.kvh,
-                        int32_t(w.k_row + int64_t(w.j0 + t) * BN), bar_k_full(s));
-          ++T;
+                        w.k_row + w.block(t) * BN, bar_k_full(s));
         }
-      }
-      // The next item, asked for only now, three blocks before this one's end: asked for at its
-      // start, a CTA with a long item would hold on to one that others are free to take (a
-      // batch of short and long sequences took 97 us instead of 78).
-      int64_t next = -1;
-      if (lane == 0 && ok) {
-        mbar_arrive_expect_tx(bar_clc, 16);
-        clc_try_cancel(resp, bar_clc);
-        if (mbar_wait_sleep(bar_clc, answers & 1, never)) {
-          next = clc_answer(resp);
-          fence_proxy_async_smem();              // read before the next answer is written
-        } else {
-          ok = false;
+        // The answer is waited for in every case: it is written into this CTA's memory.
+        if (asked) {
+          if (mbar_wait_sleep(bar_clc, answers & 1, never)) {
+            next = clc_answer(resp);
+            fence_proxy_async_smem();              // read before the next answer is written
+          } else {
+            ok = false;
+          }
         }
       }
       ++answers;
@@ -368,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
       if (*abort_flag) {                           // every load in flight lands before the CTA ends
         for (uint32_t u = T > uint32_t(C::KST) ? T - C::KST : 0; u < T; ++u)
           mbar_wait(bar_k_full(int(u % C::KST)), int(u / C::KST) & 1, never);
-        if (nq > 0) mbar_wait(bar_q, (nq - 1) & 1, never);
+        for (int u = nq > C::QST ? nq - C::QST : 0; u < nq; ++u) mbar_wait(bar_q(u % C::QST), (u / C::QST) & 1, never);
       }
     }
   } else if (warp == kVWarp) {
@@ -382,8 +400,9 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
       bool ok = true;
       for (int t = 0; ok && t < n; ++t) {
         const int s = int(T % C::VST);
-        const int64_t left = w.lk - int64_t(w.j0 + t) * BN;      // keys of the sequence from here on
-        const bool tail = left < BN;                             // at most an item's last block
+        const int j = w.block(t);
+        const int left = w.lk - j * BN;                          // keys of the sequence from here on
+        const bool tail = left < BN;                             // at most one block of an item
         if (lane == 0) {
           if (T >= uint32_t(C::VST) && !mbar_wait_sleep(bar_v_empty(s), int((T / C::VST) - 1) & 1, abort_flag)) {
             ok = false;
@@ -392,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
             mbar_arrive_expect_tx(bar, C::KV_BYTES);
             for (int c = 0; c < D / 64; ++c)
               tma_load_3d(sV + s * C::KV_BYTES + c * BN * 128, &tm_v, c * 64, w.kvh,
-                          int32_t(w.k_row + int64_t(w.j0 + t) * BN), bar);
+                          w.k_row + j * BN, bar);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -406,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
           if (!ok) break;
           for (int c = 0; c < D / 64; ++c) {
             uint8_t* rows = smem + C::OFF_V + s * C::KV_BYTES + c * BN * 128;
-            for (int x = int(left) * 8 + lane; x < BN * 8; x += 32)
+            for (int x = left * 8 + lane; x < BN * 8; x += 32)
               reinterpret_cast<uint4*>(rows)[x] = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
@@ -434,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
       if (n == 0) continue;
       bool ok = true;
       if (lane == 0) {
-        ok = mbar_wait_sleep(bar_q, nq & 1, abort_flag);
+        ok = mbar_wait_sleep(bar_q(nq % C::QST), (nq / C::QST) & 1, abort_flag);
+        const uint64_t qs = q_desc + uint64_t(((nq % C::QST) * C::Q_BYTES) >> 4);
         for (int t = 0; ok && t < n; ++t, ++T) {
           const int s = int(T % C::KST), b = int(T % C::NSB);
           if (!mbar_wait_sleep(bar_k_full(s), int(T / C::KST) & 1, abort_flag)) { ok = false; break; }
@@ -448,12 +468,12 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
           const uint32_t s_tm = tmem + C::TM_S + 128 * b;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_f16_ss(s_tm, q_desc + uint64_t(((kk / 4) * BM * 128 + (kk % 4) * 32) >> 4),
+            umma_f16_ss(s_tm, qs + uint64_t(((kk / 4) * BM * 128 + (kk % 4) * 32) >> 4),
                         ks + uint64_t(((kk / 4) * BN * 128 + (kk % 4) * 32) >> 4), C::IDESC_QK, kk > 0 ? 1u : 0u);
           umma_commit(bar_s_full(b));
           umma_commit(bar_k_empty(s));
         }
-        if (ok) umma_commit(bar_q_empty);          // Q may be replaced
+        if (ok) umma_commit(bar_q_empty(nq % C::QST));   // this Q may be replaced
       }
       ++nq;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -513,24 +533,33 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     const int tok_in = row / p.group, head_in = row - tok_in * p.group;
     const bool row_used = row < p.tok * p.group;
     uint32_t T = 0;
-    int got = 1;
+    int nq = 0;
+    bool q_pending = false;                        // O of item nq - 1 may still be read from its Q buffer
+    auto release_q = [&] {
+      if (q_pending) {
+        bulk_wait_read();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_q_empty((nq - 1) % C::QST));
+        q_pending = false;
+      }
+    };
     Item w;
-    while ((got = next_item(w)) == 1) {
+    int got = next_item(w);
+    while (got == 1) {
     const int n = w.j1 - w.j0;
-    const int64_t token = w.tok0 + tok_in;
+    const int64_t token = int64_t(w.tok0) + tok_in;
     const bool store = row_used && token < w.q_end;
-    // Keys this row sees, counted from the sequence's first key.
-    int64_t limit = w.causal ? w.lim0 + tok_in : w.lim0;
-    limit = limit > w.lk ? w.lk : limit;
+    // Keys this row sees, counted from the sequence's first key (a row past the sequence's end
+    // counts on past them; it is not stored).
+    const int limit = w.causal ? w.lim0 + (store ? tok_in : 0) : w.lim0;
     const bool sees = store && limit > 0;
     bool ok = true;
     float m_ref = -INFINITY;                       // reference max in log2 units
     float l = 0.f;                                 // this half's share of the row sum
 
-    // One key block t; false when a wait gives up.  Masked: an unseen key's weight is zero
-    // (the MUFU's 2^-inf; the polynomial would give 2^-125).
-    auto step = [&](int t, auto masked_tag) -> bool {
-      constexpr bool MASKED = decltype(masked_tag)::value;
+    // One key block t, any row's view of it; false when a wait gives up.  An unseen key's weight
+    // is zero (the MUFU's 2^-inf; the polynomial would give 2^-125).
+    auto step = [&](int t) -> bool {
       const int b = int(T % C::NSB);
       if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full(b), int(T / C::NSB) & 1, abort_flag))) return false;
       tc_fence_after();
@@ -540,12 +569,13 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
         tmem_ld_16x2_32<HALF>(tmem + lane_off + C::TM_S + 128 * b + q * 32,
                               *reinterpret_cast<uint32_t(*)[32]>(sr + q * 32));
       tmem_wait_ld();
-      if constexpr (MASKED) {
-        const int64_t left = limit - (int64_t(w.j0 + t) * BN + hf * HALF);
-        const int vis = left > HALF ? HALF : int(left < 0 ? 0 : left);
+      {
+        const int left = limit - (w.block(t) * BN + hf * HALF);
+        const int vis = left > HALF ? HALF : left < 0 ? 0 : left;
+        const uint32_t lo = vis >= 32 ? ~0u : (1u << vis) - 1u, hi = vis >= 64 ? ~0u : vis <= 32 ? 0u : (1u << (vis - 32)) - 1u;
 #pragma unroll
         for (int e = 0; e < HALF; ++e)
-          if (e >= vis) sr[e] = __float_as_uint(-INFINITY);
+          if (!(((e < 32 ? lo : hi) >> (e & 31)) & 1u)) sr[e] = __float_as_uint(-INFINITY);
       }
       float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -565,14 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
 #pragma unroll
       for (int e = 0; e < HALF / 2; ++e) {
         const uint64_t x2 = f2_fma(f2_pack_bits(sr[2 * e], sr[2 * e + 1]), c2, nm2);
-        uint64_t p2;
-        if (!MASKED && poly_pair(e)) {
-          p2 = exp2_poly_f2(x2);
-        } else {
-          float x0, x1;
-          f2_unpack(x2, x0, x1);
-          p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
-        }
+        float x0, x1;
+        f2_unpack(x2, x0, x1);
+        const uint64_t p2 = f2_pack(ex2_approx(x0), ex2_approx(x1));
         acc[e & 1] = f2_add(acc[e & 1], p2);
         float p0, p1;
         f2_unpack(p2, p0, p1);
@@ -646,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
       return 1;
     };
 
-    const int t_full = w.j_full - w.j0;
+    const int n_masked = w.j1 - w.j_full;
     int t = 0;
     const bool idle = !__any_sync(0xffffffffu, store);
     if (idle) {
@@ -657,73 +682,118 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
         if (ok && lane == 0) mbar_arrive(bar_p_full(b));
       }
     }
-    for (; ok && t < t_full; ++t, ++T) {
+    for (; ok && t < n_masked; ++t, ++T) ok = step(t);
+    release_q();                                   // the previous item's buffer, by now stored
+    for (; ok && t < n; ++t, ++T) {
       int r = 2;
       if (t > 0) r = step_spec();
       if (r == 0) ok = false;
-      else if (r == 2) ok = step(t, std::false_type{});
+      else if (r == 2) ok = step(t);
     }
-    for (; ok && t < n; ++t, ++T) ok = step(t, std::true_type{});
 
     // ---------------------------------------------------------- epilogue
+    // The next item is read while the last P V runs.
+    Item nw;
+    const int next = ok ? next_item(nw) : -1;
     if (ok && n > 0) {
       const uint32_t u = T - 1;
       ok = __all_sync(0xffffffffu, mbar_wait(bar_o_done(int(u % C::NSB)), int(u / C::NSB) & 1, abort_flag));
       tc_fence_after();
     }
     if (!ok) { got = -1; break; }
-    uint32_t ov[DH] = {};
-    if (n > 0) {
-#pragma unroll
-      for (int q = 0; q < DH / 32; ++q)
-        tmem_ld_16x2_32<DH>(tmem + lane_off + C::TM_O + q * 32, *reinterpret_cast<uint32_t(*)[32]>(ov + q * 32));
-      tmem_wait_ld();
-      // O is in registers: the next item's first P V may overwrite it.
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_o_free);
-    }
     const float l_row = l + __shfl_xor_sync(0xffffffffu, l, 16);
     const bool none = !sees || l_row == 0.f;       // a NaN sum goes through as NaN
-    const float inv_l = none ? 0.f : 1.f / l_row;
+    const float inv_l = none ? 0.f : __fdividef(1.f, l_row);
     const int head = w.kvh * p.group + head_in;
     const int64_t part_row = ((int64_t(w.split) * p.kv_heads + w.kvh) * p.total_q + token) * p.group + head_in;
-    if (store) {
-      if (p.splits > 0) {
-        float* dst = p.part_o + part_row * D + hf * DH;
-#pragma unroll
-        for (int e4 = 0; e4 < DH / 4; ++e4) {
-          float4 f;
-          f.x = none ? 0.f : __uint_as_float(ov[4 * e4]) * inv_l;
-          f.y = none ? 0.f : __uint_as_float(ov[4 * e4 + 1]) * inv_l;
-          f.z = none ? 0.f : __uint_as_float(ov[4 * e4 + 2]) * inv_l;
-          f.w = none ? 0.f : __uint_as_float(ov[4 * e4 + 3]) * inv_l;
-          reinterpret_cast<float4*>(dst)[e4] = f;
+    // Rows go out through this item's Q buffer (its Q K^T is done), a warp's 16 rows in the tensor
+    // maps' 128-byte swizzle, so staging meets no bank conflict.  When all 16 are rows of the
+    // sequence and whole tokens (the group divides 16) one lane stores them as a box per 64
+    // columns, asynchronously: an item's epilogue 2,900 -> 1,000 cycles against stores of half
+    // rows from registers.  (A copy per row, issued by 32 lanes, took 2,500 cycles to issue.)
+    constexpr int UNITS = D / 8, HU = UNITS / 2;    // 16-byte units of a row, of a half row
+    const int r16 = lane & 15;
+    const uint32_t stage_off = C::OFF_Q + (nq % C::QST) * C::Q_BYTES + (warp - kSoftmaxWarp0) * 16 * D * 2;
+    if (n > 0) {
+#pragma unroll 1
+      for (int q = 0; q < DH / 32; ++q) {
+        uint32_t ov[32];
+        tmem_ld_16x2_32<DH>(tmem + lane_off + C::TM_O + q * 32, ov);
+        tmem_wait_ld();
+        if (q == DH / 32 - 1) {
+          // O is in registers: the next item's first P V may overwrite it.
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_o_free);
         }
-      } else {
-        __nv_bfloat16* dst = p.o + token * p.o_token + int64_t(head) * p.o_head + hf * DH;
-        uint32_t wv[DH / 2];
+        if (p.splits > 0) {
+          if (store) {
+            float* dst = p.part_o + part_row * D + hf * DH + q * 32;
 #pragma unroll
-        for (int e = 0; e < DH / 2; ++e)
-          wv[e] = none ? 0u : pack_bf16x2(__uint_as_float(ov[2 * e]) * inv_l, __uint_as_float(ov[2 * e + 1]) * inv_l);
-        if (p.o_align32) {
-#pragma unroll
-          for (int e8 = 0; e8 < DH / 16; ++e8)
-            st_global_v8(dst + e8 * 16, *reinterpret_cast<const uint32_t(*)[8]>(wv + e8 * 8));
+            for (int e4 = 0; e4 < 8; ++e4) {
+              float4 f;
+              f.x = none ? 0.f : __uint_as_float(ov[4 * e4]) * inv_l;
+              f.y = none ? 0.f : __uint_as_float(ov[4 * e4 + 1]) * inv_l;
+              f.z = none ? 0.f : __uint_as_float(ov[4 * e4 + 2]) * inv_l;
+              f.w = none ? 0.f : __uint_as_float(ov[4 * e4 + 3]) * inv_l;
+              reinterpret_cast<float4*>(dst)[e4] = f;
+            }
+          }
+          __syncwarp();
         } else {
 #pragma unroll
-          for (int e4 = 0; e4 < DH / 8; ++e4)
-            reinterpret_cast<uint4*>(dst)[e4] = make_uint4(wv[4 * e4], wv[4 * e4 + 1], wv[4 * e4 + 2], wv[4 * e4 + 3]);
+          for (int u = 0; u < 4; ++u) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = none ? 0u : pack_bf16x2(__uint_as_float(ov[8 * u + 2 * e]) * inv_l, __uint_as_float(ov[8 * u + 2 * e + 1]) * inv_l);
+            const int unit = hf * HU + q * 4 + u;
+            *reinterpret_cast<uint4*>(smem + stage_off + (unit / 8) * 2048 + r16 * 128 + (((unit ^ r16) & 7) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
+          }
         }
       }
-      if (hf == 0) {
-        const float lse2 = none ? -INFINITY : m_ref + __log2f(l_row);
-        if (p.splits > 0) p.part_lse[part_row] = lse2;
-        else p.lse[int64_t(head) * p.total_q + token] = lse2 * kLn2;
+      if (p.splits == 0) {
+        if (__all_sync(0xffffffffu, store) && p.o_boxes) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            for (int c64 = 0; c64 < D / 64; ++c64)
+              tma_store_3d(&tm_o, s_base + stage_off + c64 * 2048, c64 * 64, w.kvh * p.group, int32_t(token));
+            bulk_commit();
+          }
+        } else {
+          __syncwarp();
+          const int64_t off = store ? token * p.o_token + int64_t(head) * p.o_head : int64_t(-1);
+          const int unit = lane % UNITS;
+#pragma unroll 1
+          for (int r0 = 0; r0 < 16; r0 += 32 / UNITS) {
+            const int r = r0 + lane / UNITS;
+            const int64_t at = __shfl_sync(0xffffffffu, off, r);
+            const uint4 v = *reinterpret_cast<const uint4*>(smem + stage_off + (unit / 8) * 2048 + r * 128 + (((unit ^ r) & 7) << 4));
+            if (at >= 0) *reinterpret_cast<uint4*>(p.o + at + unit * 8) = v;
+          }
+          fence_proxy_async_smem();                // read before the buffer's next TMA write
+        }
       }
+      ++nq;
+      q_pending = true;
+    } else if (store) {
+      // No key for any row: O = 0 (this item has no Q buffer).
+      uint4* dst = reinterpret_cast<uint4*>(p.o + token * p.o_token + int64_t(head) * p.o_head + hf * DH);
+#pragma unroll 1
+      for (int e = 0; e < DH / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (store && hf == 0) {
+      const float lse2 = none ? -INFINITY : m_ref + __log2f(l_row);
+      if (p.splits > 0) p.part_lse[part_row] = lse2;
+      else p.lse[int64_t(head) * p.total_q + token] = lse2 * kLn2;
     }
     __syncwarp();                                  // the next item's loads are the whole warp's
+    w = nw;
+    got = next;
     }
+    bulk_wait_read();                              // shared memory outlives the copies from it
     if (got < 0) {
       *abort_flag = 1;
       if (lane == 0) report_fault(p.err, 5, 26);
@@ -742,17 +812,20 @@ template <int D>
 cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why) {
   using C = Cfg<D>;
   const int group = a.q_heads / a.kv_heads, tok = BM / group;
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
+  const bool boxes = a.splits == 0 && 16 % group == 0;
   // Without keys nothing is loaded: the maps then describe Q's rows.
   const bool keys = a.total_k > 0;
   if (!make_heads_map(&tq, a.q, a.total_q, a.q_heads, D, a.q_token, a.q_head, group, tok) ||
       !make_heads_map(&tk, keys ? a.k : a.q, keys ? a.total_k : a.total_q, keys ? a.kv_heads : a.q_heads, D,
                       keys ? a.k_token : a.q_token, keys ? a.k_head : a.q_head, 1, BN) ||
       !make_heads_map(&tv, keys ? a.v : a.q, keys ? a.total_k : a.total_q, keys ? a.kv_heads : a.q_heads, D,
-                      keys ? a.v_token : a.q_token, keys ? a.v_head : a.q_head, 1, BN)) {
+                      keys ? a.v_token : a.q_token, keys ? a.v_head : a.q_head, 1, BN) ||
+      (boxes && !make_heads_map(&to, a.o, a.total_q, a.q_heads, D, a.o_token, a.o_head, group, 16 / group))) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }
+  if (!boxes) to = tq;                             // not used
   static DeviceFlags attr_set = {};
   cudaError_t e = once_per_device(attr_set, [] {
     return cudaFuncSetAttribute(packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
@@ -773,13 +846,13 @@ cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why)
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
-  p.o_align32 = ((reinterpret_cast<uintptr_t>(a.o) & 31) == 0 && a.o_token % 16 == 0 && a.o_head % 16 == 0) ? 1 : 0;
+  p.o_boxes = boxes ? 1 : 0;
   p.splits = a.splits;
   p.part_o = a.part_o;
   p.part_lse = a.part_lse;
   p.err = a.err;
   const int64_t tiles = a.splits > 0 ? (a.total_q + tok - 1) / tok * a.splits : a.total_q / tok + a.num_seqs;
-  packed_attn_kernel<D><<<dim3(unsigned(tiles * a.kv_heads)), kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, p);
+  packed_attn_kernel<D><<<dim3(unsigned(tiles * a.kv_heads)), kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
   return cudaGetLastError();
 }
 
