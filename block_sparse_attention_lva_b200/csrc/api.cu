@@ -476,18 +476,21 @@ lva_status lva_packed_attn(const lva_packed_params* p, const void* q, const void
   return ok();
 }
 
-// Parts of the prefix: as many as shorten the longest CTA's walk.  With c = items * parts CTAs
-// on 148 SMs the pass takes about ceil(c / 148) * (ceil(blocks / parts) + 2) block times, the 2
-// for a part's start and end; parts past 32 would cost more in joining than they gain.
+// Parts of the prefix.  In block times (128 rows by 128 keys), with c = items * parts CTAs on
+// 148 SMs, the pass takes about blocks / parts when c <= 148, or items * blocks / 148 and half a
+// part of tail when there are more, and in either case 3 for a part's start and end; a part's
+// rows cost the join their bytes, written and read (about 7.2 MB a block time).
 static int prefix_parts(const lva_shared_prefix_params* p) {
   if (p->prefix_len == 0) return 0;
   const int tok = 128 / (p->q_heads / p->kv_heads);
-  const int64_t items = (int64_t(p->B) * p->steps + tok - 1) / tok * p->kv_heads;
+  const double items = double((int64_t(p->B) * p->steps + tok - 1) / tok * p->kv_heads);
   const int64_t blocks = (p->prefix_len + 127) / 128;
+  const double join = double(p->B) * p->steps * p->q_heads * (p->d * 8 + 8) / 7.2e6;
   int best = 1;
-  int64_t best_cost = 0;
+  double best_cost = 0;
   for (int s = 1; s <= 32 && s <= blocks; ++s) {
-    const int64_t cost = (items * s + 147) / 148 * ((blocks + s - 1) / s + 2);
+    const double part = double((blocks + s - 1) / s), load = items * s / 148;
+    const double cost = (load <= 1 ? part : items * blocks / 148 + part / 2) + 3 * (load > 1 ? load : 1) + join * s;
     if (s == 1 || cost < best_cost) { best = s; best_cost = cost; }
   }
   return best;
@@ -566,6 +569,16 @@ lva_status lva_shared_prefix_attn(const lva_shared_prefix_params* p, const void*
   float* part_o = reinterpret_cast<float*>(ws + w.part_o);
   float* part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   const char* why = "launch";
+  CacheAttnArgs c{q, k_cache, v_cache, lens, o, lse, p->capacity > 0 ? weight : nullptr, p->B, p->steps, p->q_heads,
+                  p->kv_heads, p->d, p->prefix_len, p->capacity, p->q_token_stride, p->q_head_stride,
+                  p->o_token_stride, p->o_head_stride, p->scale, w.parts, part_o, part_lse,
+                  reinterpret_cast<float*>(ws + w.own_o), reinterpret_cast<float*>(ws + w.own_lse),
+                  weight != nullptr ? reinterpret_cast<float*>(ws + w.scores) : nullptr, w.score_stride,
+                  kCacheWorkers, err};
+  if (p->capacity > 0) {
+    const cudaError_t e = launch_cache_attn(c, stream, &why);
+    if (e != cudaSuccess) return fail(LVA_ERR_CUDA, "shared_prefix: %s: %s", why, cudaGetErrorString(e));
+  }
   if (w.parts > 0) {
     PackedArgs a{q, prefix_k, prefix_v, nullptr, nullptr, 1, p->q_heads, p->kv_heads, p->d,
                  int64_t(p->B) * p->steps, p->prefix_len,
@@ -573,15 +586,6 @@ lva_status lva_shared_prefix_attn(const lva_shared_prefix_params* p, const void*
                  p->v_token_stride, p->v_head_stride, 0, 0, nullptr, nullptr, 0, p->scale,
                  w.parts, part_o, part_lse, err};
     const cudaError_t e = launch_packed(a, stream, &why);
-    if (e != cudaSuccess) return fail(LVA_ERR_CUDA, "shared_prefix: %s: %s", why, cudaGetErrorString(e));
-  }
-  CacheAttnArgs c{q, k_cache, v_cache, lens, o, lse, p->capacity > 0 ? weight : nullptr, p->B, p->steps, p->q_heads,
-                  p->kv_heads, p->d, p->prefix_len, p->capacity, p->q_token_stride, p->q_head_stride,
-                  p->o_token_stride, p->o_head_stride, p->scale, w.parts, part_o, part_lse,
-                  reinterpret_cast<float*>(ws + w.own_o), reinterpret_cast<float*>(ws + w.own_lse),
-                  weight != nullptr ? reinterpret_cast<float*>(ws + w.scores) : nullptr, w.score_stride, err};
-  if (p->capacity > 0) {
-    const cudaError_t e = launch_cache_attn(c, stream, &why);
     if (e != cudaSuccess) return fail(LVA_ERR_CUDA, "shared_prefix: %s: %s", why, cudaGetErrorString(e));
   }
   return from_cuda(launch_cache_join(c, stream), "shared_prefix join launch");

@@ -220,12 +220,14 @@ struct CacheAttnArgs {
   float* own_lse;            // [slots, group * steps], log2 units
   float* scores;             // NULL or [B, kv_heads, group * steps, score_stride]
   int64_t score_stride;
+  int workers;               // CTAs of the cache pass, at most kCacheWorkers
   int* err;
 };
 // Most rows (query heads per key/value head x tokens per step) of one sequence.
 constexpr int kCacheMaxRows = 64;
-// Segments that the cache pass writes at most: one per (sequence, head) and one per worker.
-constexpr int kCacheWorkers = 296;
+// Most workers (CTAs) of the cache pass; it leaves at most one segment per (sequence, head) and
+// one per worker.
+constexpr int kCacheWorkers = 148;
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream, const char** why);
 cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream);
 

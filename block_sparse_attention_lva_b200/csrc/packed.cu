@@ -339,14 +339,16 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
       // are free to take (a batch of short and long sequences took 97 us instead of 78).
       if (lane == 0 && ok) {
         const int t_ask = n > kAhead ? n - kAhead : 0;
+        bool asked = false;
         auto ask = [&] {
+          if (p.splits > 0) return;                // parts of a prefix are alike: one to a CTA
           mbar_arrive_expect_tx(bar_clc, 16);
           clc_try_cancel(resp, bar_clc);
+          asked = true;
         };
         if (n == 0) ask();
-        bool asked = n == 0;
         for (int t = 0; ok && t < n; ++t, ++T) {
-          if (t == t_ask) { ask(); asked = true; }
+          if (t == t_ask) ask();
           if (t == 0) {
             // Q's buffer is free once the item before the previous one has been stored.
             const int s = nq % C::QST;
@@ -375,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
           } else {
             ok = false;
           }
+          ++answers;
         }
       }
-      ++answers;
       bid = __shfl_sync(0xffffffffu, next, 0);
       ok = __shfl_sync(0xffffffffu, ok, 0);
     }
@@ -852,7 +854,8 @@ cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why)
   p.part_lse = a.part_lse;
   p.err = a.err;
   const int64_t tiles = a.splits > 0 ? (a.total_q + tok - 1) / tok * a.splits : a.total_q / tok + a.num_seqs;
-  packed_attn_kernel<D><<<dim3(unsigned(tiles * a.kv_heads)), kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
+  const unsigned blocks = unsigned(tiles * a.kv_heads);
+  packed_attn_kernel<D><<<blocks, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
   return cudaGetLastError();
 }
 
