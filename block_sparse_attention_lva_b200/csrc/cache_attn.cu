@@ -67,13 +67,19 @@ __device__ __forceinline__ int live_len(const int32_t* lens, int b, int64_t capa
 }
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
 
-// Tiles of one head of all sequences, and of those before `stop` (whole warp).  Tiles of all
-// planes stay below 2^31: B * kv_heads * capacity and B * kv_heads do.
-__device__ __forceinline__ int count_tiles(const int32_t* lens, int B, int64_t capacity, int stop, int* before) {
+// A plane counts as its tiles and kSegment more: what a segment's start and end (its first
+// loads' latency, the join of its parts) cost beside its tiles.  Without it a worker with many
+// planes of a tile each took three times as long as the others (47 us instead of 16).
+constexpr int kSegment = 2;
+__device__ __forceinline__ int plane_cost(int tiles) { return tiles > 0 ? tiles + kSegment : 0; }
+
+// Cost of one head of all sequences, and of those before `stop` (whole warp).  All planes'
+// costs stay below 2^31: B * kv_heads * capacity / 64 and three times B * kv_heads do.
+__device__ __forceinline__ int count_cost(const int32_t* lens, int B, int64_t capacity, int stop, int* before) {
   const int lane = threadIdx.x & 31;
   int all = 0, part = 0;
   for (int b = lane; b < B; b += 32) {
-    const int t = tiles_of(live_len(lens, b, capacity));
+    const int t = plane_cost(tiles_of(live_len(lens, b, capacity)));
     all += t;
     if (b < stop) part += t;
   }
@@ -81,8 +87,8 @@ __device__ __forceinline__ int count_tiles(const int32_t* lens, int B, int64_t c
   return __reduce_add_sync(kFull, all);
 }
 
-// A list of `total` tiles in runs for up to `workers` workers: the first `total` mod n of the
-// n = min(workers, total) runs are one tile longer, and none of the n is empty.
+// A list of `total` places in runs for up to `workers` workers: the first `total` mod n of the
+// n = min(workers, total) runs are one place longer, and none of the n is empty.
 struct Runs {
   int n, len, longer;
   __device__ __forceinline__ Runs(int total, int workers) {
@@ -91,30 +97,31 @@ struct Runs {
     longer = total - n * len;
   }
   __device__ __forceinline__ int start(int w) const { return w * len + (w < longer ? w : longer); }
-  __device__ __forceinline__ int worker(int x) const {           // whose run holds tile x (n > 0)
+  __device__ __forceinline__ int worker(int x) const {           // whose run holds place x (n > 0)
     const int split = longer * (len + 1);
     return x < split ? int(uint32_t(x) / uint32_t(len + 1)) : longer + int(uint32_t(x - split) / uint32_t(len));
   }
 };
 
-// Walks a worker's run plane by plane (every warp the same walk).
+// Walks a worker's run plane by plane (every warp the same walk).  A plane's tiles come first in
+// its part of the list; a run that meets only the rest of it has no tile there.
 struct Walk {
   const CacheParams& p;
-  int left;                  // tiles of the run not yet handed out
+  int left;                  // of the run, not yet handed out
   int b, kvh, n, tiles, t0;  // the current plane, its first tile of the run
   __device__ __forceinline__ Walk(const CacheParams& params, int worker) : p(params) {
     const int lane = threadIdx.x & 31;
     int unused;
-    const Runs runs(count_tiles(p.lens, p.B, p.capacity, 0, &unused) * p.kv_heads, p.workers);
+    const Runs runs(count_cost(p.lens, p.B, p.capacity, 0, &unused) * p.kv_heads, p.workers);
     left = 0;
     b = kvh = n = tiles = t0 = 0;
     if (worker >= runs.n) return;
     int at = runs.start(worker);
     left = runs.start(worker + 1) - at;
-    // the sequence that holds tile `at`: 32 sequences at a time
+    // the sequence that holds place `at`: 32 sequences at a time
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int mine = b0 + lane < p.B ? live_len(p.lens, b0 + lane, p.capacity) : 0;
-      const int own = tiles_of(mine) * p.kv_heads;
+      const int own = plane_cost(tiles_of(mine)) * p.kv_heads;
       int sum = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -128,18 +135,19 @@ struct Walk {
         n = __shfl_sync(kFull, mine, l);
         const int in = at - __shfl_sync(kFull, sum - own, l);
         tiles = tiles_of(n);
-        kvh = int(uint32_t(in) / uint32_t(tiles));
-        t0 = in - kvh * tiles;
+        kvh = int(uint32_t(in) / uint32_t(plane_cost(tiles)));
+        t0 = in - kvh * plane_cost(tiles);
+        if (t0 >= tiles) next();                   // starts behind this plane's tiles
         return;
       }
       at -= __shfl_sync(kFull, sum, 31);
     }
     left = 0;                // not reached: the run lies inside the list
   }
-  // Tiles of the current plane in this run.
+  // Tiles of the current plane in this run; at least one while left > 0.
   __device__ __forceinline__ int count() const { return left < tiles - t0 ? left : tiles - t0; }
   __device__ __forceinline__ void next() {
-    left -= count();
+    left -= plane_cost(tiles) - t0;
     t0 = 0;
     if (left <= 0) return;
     if (++kvh < p.kv_heads) return;
@@ -156,9 +164,8 @@ struct Walk {
 // NT: 8-row tiles a warp holds; WR: row parts, each a warp's.  Up to 8 * NT * WR rows.
 template <int D, int NT, int WR>
 struct Cfg {
-  // consumer warps: as many as their registers allow (four or three warps a scheduler, with
-  // the producer)
-  static constexpr int WARPS = NT == 1 ? 12 : 8;
+  // consumer warps: with the producer three a scheduler, 168 registers a thread
+  static constexpr int WARPS = NT == 1 ? 10 : 8;
   static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int GROUP_WARPS = WR > 2 ? WR : 2;
   static constexpr int GROUPS = WARPS / GROUP_WARPS;  // they take the tiles in turn
@@ -168,22 +175,23 @@ struct Cfg {
   static constexpr int WROWS = 8 * NT;
   static constexpr int QROWS = WROWS * WR;
   static constexpr int SLOT = kTile * D * 2;          // one K or V tile
-  // Ring: 192 KB in flight per SM (128 KB with more rows, for their join); 128 KB reach the
-  // full HBM rate even on half of the SMs.  A slot's tiles must all go to one group: its parity
+  // Ring: 160 KB in flight per SM (128 KB with more rows, for their join); 64 KB reach the full
+  // HBM rate when all SMs load.  A slot's tiles must all go to one group: its parity
   // wait for a tile is then preceded by its own wait for the slot's tile before.  (A group that
   // waits on a slot whose tile before, another group's, has not landed finds the parity of the
   // tile before that and passes.)
-  static constexpr int NSLOT = (NT == 1 ? 12 : 8) * (128 / D);
+  static constexpr int NSLOT = (NT == 1 ? 10 : 8) * (128 / D);
   static_assert(NSLOT / 2 % GROUPS == 0, "a slot belongs to one group");
   static constexpr int Q_SLOT = QROWS * D * 2;
   static constexpr int FRAG = D / 16 * NT * 4;        // O registers per lane
   static constexpr int STAT = 4 * NT;                 // m, l
-  static constexpr int JOIN = (PARTS + 1) / 2 * WR * (FRAG + STAT) * 32 * 4;
+  static constexpr int JOIN = PARTS * WR * (FRAG + STAT) * 32 * 4;
   static constexpr int OFF_KV = 0;
   static constexpr int OFF_Q = OFF_KV + NSLOT * SLOT;
-  static constexpr int OFF_JOIN = OFF_Q + 2 * Q_SLOT;
+  static constexpr int QS = WR == 4 ? 1 : 2;          // Q slots
+  static constexpr int OFF_JOIN = OFF_Q + QS * Q_SLOT;
   static constexpr int OFF_BAR = OFF_JOIN + JOIN;
-  static constexpr int B_F = 0, B_E = NSLOT, B_QF = 2 * NSLOT, B_QE = B_QF + 2, B_GRP = B_QE + 2, NUM_BARS = B_GRP + 2;
+  static constexpr int B_F = 0, B_E = NSLOT, B_QF = 2 * NSLOT, B_QE = B_QF + QS, B_GRP = B_QE + QS, NUM_BARS = B_GRP + 2;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16;
   // more than half of an SM, so that the workers spread over the SMs one by one
@@ -240,22 +248,19 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
       if (n < 0 || int64_t(n) > p.capacity) report_fault(p.err, 1, b);
     }
   // Q rows past the group's are never loaded: zero, so that no stray value is computed with.
-  for (int x = threadIdx.x; x < 2 * C::Q_SLOT / 16; x += C::THREADS)
+  for (int x = threadIdx.x; x < C::QS * C::Q_SLOT / 16; x += C::THREADS)
     reinterpret_cast<uint4*>(smem + C::OFF_Q)[x] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NSLOT; ++s) { mbar_init(bar_full(s), 1); mbar_init(bar_empty(s), C::GROUP_WARPS); }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(bar_q_full(s), 1);
-      mbar_init(bar_q_empty(s), C::WARPS);
-      mbar_init(bar0 + 8u * (C::B_GRP + s), C::WARPS);
-    }
+    for (int s = 0; s < C::QS; ++s) { mbar_init(bar_q_full(s), 1); mbar_init(bar_q_empty(s), C::WARPS); }
+    for (int s = 0; s < 2; ++s) mbar_init(bar0 + 8u * (C::B_GRP + s), C::WARPS);
     *abort_flag = 0;
     *never = 0;
     mbar_fence_init();
   }
-  __syncthreads();
   Walk walk(p, worker);
+  __syncthreads();
 
   if (warp == C::WARPS) {
     // ------------------------------------------------------------ TMA producer
@@ -265,8 +270,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
     if (lane == 0 && walk.left > 0) { tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v); }
     for (; ok && walk.left > 0; walk.next(), ++seg) {
       if (lane == 0) {
-        const int qs = int(seg & 1);
-        ok = seg < 2 || mbar_wait_sleep(bar_q_empty(qs), ((seg >> 1) - 1) & 1, abort_flag);
+        const int qs = int(seg % C::QS);
+        ok = seg < C::QS || mbar_wait_sleep(bar_q_empty(qs), ((seg / C::QS) - 1) & 1, abort_flag);
         if (ok) {
           mbar_arrive_expect_tx(bar_q_full(qs), uint32_t(p.rows * D * 2));
           for (int c = 0; c < D / 64; ++c)
@@ -301,7 +306,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
     if (lane == 0 && *abort_flag) {               // every load in flight lands before the CTA ends
       for (uint32_t x = u > uint32_t(C::NSLOT) ? u - C::NSLOT : 0; x < u; ++x)
         mbar_wait(bar_full(int(x % C::NSLOT)), (x / C::NSLOT) & 1, never);
-      for (uint32_t x = loaded_q > 2 ? loaded_q - 2 : 0; x < loaded_q; ++x) mbar_wait(bar_q_full(int(x & 1)), (x >> 1) & 1, never);
+      for (uint32_t x = loaded_q > C::QS ? loaded_q - C::QS : 0; x < loaded_q; ++x)
+        mbar_wait(bar_q_full(int(x % C::QS)), (x / C::QS) & 1, never);
     }
   } else {
     // ------------------------------------------------------------ consumers
@@ -329,8 +335,8 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
     auto sw = [](uint32_t chunk, int r, int unit) { return chunk + r * 128 + ((unit ^ (r & 7)) << 4); };
 
     for (; ok && walk.left > 0; walk.next(), ++seg) {
-      const int qs = int(seg & 1);
-      ok = __all_sync(kFull, mbar_wait_sleep(bar_q_full(qs), (seg >> 1) & 1, abort_flag));
+      const int qs = int(seg % C::QS);
+      ok = __all_sync(kFull, mbar_wait_sleep(bar_q_full(qs), (seg / C::QS) & 1, abort_flag));
       if (!ok) break;
       uint32_t qf[D / 16][NT][2];                  // Q^T fragments
       {
@@ -367,6 +373,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
       }
       const int64_t plane = int64_t(walk.b) * p.kv_heads + walk.kvh;
       const int cnt = walk.count();
+      const int group0 = int(T % C::GROUPS);       // of the segment's first tile
       for (int t = 0; t < cnt; ++t, ++T) {
         if (int(T % C::GROUPS) != group) continue;
         const int tile0 = (walk.t0 + t) * kTile;                   // the tile's first key
@@ -504,86 +511,76 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
       }
       if (!ok) break;
 
-      // Row sums over the lanes of a column pair; then the parts meet, upper half into lower.
+      // Row sums over the lanes of a column pair; then the parts meet in shared memory: each that
+      // had a tile leaves (O, m, l) there, and the parts' warps share out the 16-dim pieces.
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) l[nt][e] += __shfl_xor_sync(kFull, l[nt][e], o);
-      {
-        auto slot = [&](int i) {
-          return reinterpret_cast<float*>(smem + C::OFF_JOIN) + (i * WR + wr) * (C::FRAG + C::STAT) * 32 + lane;
-        };
-        auto put = [&](int i) {
-          float* s = slot(i);
+      auto slot = [&](int i) {
+        return reinterpret_cast<float*>(smem + C::OFF_JOIN) + (i * WR + wr) * (C::FRAG + C::STAT) * 32 + lane;
+      };
+      auto has_tile = [&](int i) {
+        const int after = i / C::WK - group0;      // groups take tiles in turn, from group0 on
+        return (after < 0 ? after + C::GROUPS : after) < cnt;
+      };
+      ok = group_sync();                           // the previous segment's pieces have been read
+      if (!ok) break;
+      if (has_tile(part)) {
+        float* s = slot(part);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int x = 0; x < D / 16; ++x)
+          for (int x = 0; x < D / 16; ++x)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[((nt * (D / 16) + x) * 4 + e) * 32] = of[x][nt][e];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              s[(C::FRAG + nt * 4 + e) * 32] = m[nt][e];
-              s[(C::FRAG + nt * 4 + 2 + e) * 32] = l[nt][e];
-            }
-          }
-        };
-        auto add = [&](int i) {
-          const float* s = slot(i);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float n = s[(C::FRAG + nt * 4 + e) * 32], t = fmaxf(m[nt][e], n);
-              const float u = t == -INFINITY ? 0.f : t;
-              const float x = ex2_approx(m[nt][e] - u), y = ex2_approx(n - u);
-              l[nt][e] = l[nt][e] * x + s[(C::FRAG + nt * 4 + 2 + e) * 32] * y;
-              m[nt][e] = t;
-#pragma unroll
-              for (int i2 = 0; i2 < D / 16; ++i2) {
-                of[i2][nt][e] = of[i2][nt][e] * x + s[((nt * (D / 16) + i2) * 4 + e) * 32] * y;
-                of[i2][nt][e + 2] = of[i2][nt][e + 2] * x + s[((nt * (D / 16) + i2) * 4 + e + 2) * 32] * y;
-              }
-            }
-        };
-        // Of n parts the upper n / 2 are added to the lowest.  In the first round part h + i uses
-        // slot i; later a part writes to the slot of its own number, which only it may have read,
-        // so one sync a round and one at the end are enough.
-        bool first = true;
-#pragma unroll 1
-        for (int n = C::PARTS; n > 1;) {
-          const int h = (n + 1) / 2;
-          if (part >= h && part < n) put(first ? part - h : part);
-          ok = group_sync();
-          if (!ok) break;
-          if (part < n - h) add(first ? part : part + h);
-          first = false;
-          n = h;
-        }
-        ok = ok && group_sync();                   // the slots may be written again
-        if (!ok) break;
-      }
-      if (part == 0) {
-        const int64_t at = (plane + worker) * p.rows;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int e = 0; e < 4; ++e) s[((nt * (D / 16) + x) * 4 + e) * 32] = of[x][nt][e];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int row = row_of(nt, e);
-            if (row < p.rows) {
-              const bool none = l[nt][e] == 0.f;   // a NaN sum goes through as NaN
-              const float inv = none ? 0.f : 1.f / l[nt][e];
-              float* dst = p.own_o + (at + row) * D + g;
-#pragma unroll
-              for (int x = 0; x < D / 16; ++x) {
-                dst[x * 16] = none ? 0.f : of[x][nt][e] * inv;
-                dst[x * 16 + 8] = none ? 0.f : of[x][nt][e + 2] * inv;
-              }
-              if (g == 0) p.own_lse[at + row] = none ? -INFINITY : m[nt][e] + __log2f(l[nt][e]);
-            }
+            s[(C::FRAG + nt * 4 + e) * 32] = m[nt][e];
+            s[(C::FRAG + nt * 4 + 2 + e) * 32] = l[nt][e];
           }
+        }
+      }
+      ok = group_sync();
+      if (!ok) break;
+      const int64_t at = (plane + worker) * p.rows;
+#pragma unroll 1
+      for (int piece = part; piece < NT * (D / 16); piece += C::PARTS) {
+        const int nt = piece / (D / 16), x = piece - nt * (D / 16);
+        float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < C::PARTS; ++i)
+          if (has_tile(i)) {
+            top[0] = fmaxf(top[0], slot(i)[(C::FRAG + nt * 4) * 32]);
+            top[1] = fmaxf(top[1], slot(i)[(C::FRAG + nt * 4 + 1) * 32]);
+          }
+        const float use[2] = {top[0] == -INFINITY ? 0.f : top[0], top[1] == -INFINITY ? 0.f : top[1]};
+#pragma unroll
+        for (int i = 0; i < C::PARTS; ++i)
+          if (has_tile(i)) {
+            const float* s = slot(i);
+            const float w0 = ex2_approx(s[(C::FRAG + nt * 4) * 32] - use[0]), w1 = ex2_approx(s[(C::FRAG + nt * 4 + 1) * 32] - use[1]);
+            sum[0] = fmaf(w0, s[(C::FRAG + nt * 4 + 2) * 32], sum[0]);
+            sum[1] = fmaf(w1, s[(C::FRAG + nt * 4 + 3) * 32], sum[1]);
+            acc[0] = fmaf(w0, s[(piece * 4) * 32], acc[0]);
+            acc[1] = fmaf(w1, s[(piece * 4 + 1) * 32], acc[1]);
+            acc[2] = fmaf(w0, s[(piece * 4 + 2) * 32], acc[2]);
+            acc[3] = fmaf(w1, s[(piece * 4 + 3) * 32], acc[3]);
+          }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = row_of(nt, e);
+          if (row < p.rows) {
+            const bool none = sum[e] == 0.f;       // a NaN sum goes through as NaN
+            const float inv = none ? 0.f : __fdividef(1.f, sum[e]);
+            float* dst = p.own_o + (at + row) * D + x * 16 + g;
+            dst[0] = none ? 0.f : acc[e] * inv;
+            dst[8] = none ? 0.f : acc[e + 2] * inv;
+            if (x == 0 && g == 0) p.own_lse[at + row] = none ? -INFINITY : top[e] + __log2f(sum[e]);
+          }
+        }
       }
       __syncwarp();
     }
@@ -636,7 +633,7 @@ __device__ __forceinline__ Parts parts_of(const JoinParams& p, int b, int kvh, i
   x.own0 = 0;
   const int tiles = tiles_of(n);
   if (tiles > 0) {
-    const int s0 = before * p.kv_heads + kvh * tiles;
+    const int s0 = before * p.kv_heads + kvh * plane_cost(tiles);
     const int w0 = runs.worker(s0), w1 = runs.worker(s0 + tiles - 1);
     x.own0 = (int64_t(b) * p.kv_heads + kvh + w0) * p.rows + r;
     x.count += w1 - w0 + 1;
@@ -681,7 +678,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
     int before = 0, total = 0, n = 0;
     if (p.workers > 0) {
       n = live_len(p.lens, b, p.capacity);
-      total = count_tiles(p.lens, p.B, p.capacity, b, &before) * p.kv_heads;
+      total = count_cost(p.lens, p.B, p.capacity, b, &before) * p.kv_heads;
     }
     const Parts x = parts_of(p, b, kvh, r, n, Runs(total, p.workers), before);
     const int t = r / p.group, head = kvh * p.group + (r - t * p.group);
@@ -750,7 +747,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
   const int n = live_len(p.lens, b, p.capacity);
   if (chunk * kChunk >= n) return;
   int before = 0;
-  const int total = count_tiles(p.lens, p.B, p.capacity, b, &before) * p.kv_heads;
+  const int total = count_cost(p.lens, p.B, p.capacity, b, &before) * p.kv_heads;
   const Runs runs(total, p.workers);
   for (int r = warp; r < p.rows; r += kJoinThreads / 32) {
     const float lse = join_lse(p, parts_of(p, b, kvh, r, n, runs, before));
