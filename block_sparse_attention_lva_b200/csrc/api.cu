@@ -469,7 +469,7 @@ lva_status lva_packed_attn(const lva_packed_params* p, const void* q, const void
   PackedArgs a{q, k, v, o, lse, p->num_seqs, p->q_heads, p->kv_heads, p->d, p->total_q, p->total_k,
                p->q_token_stride, p->q_head_stride, p->k_token_stride, p->k_head_stride,
                p->v_token_stride, p->v_head_stride, p->o_token_stride, p->o_head_stride,
-               cu_q, cu_k, p->causal != 0, p->scale, 0, nullptr, nullptr, err};
+               cu_q, cu_k, p->causal != 0, p->scale, 0, nullptr, nullptr, 0, err};
   const char* why = "launch";
   const cudaError_t e = launch_packed(a, stream, &why);
   if (e != cudaSuccess) return fail(LVA_ERR_CUDA, "packed: %s: %s", why, cudaGetErrorString(e));
@@ -584,7 +584,7 @@ lva_status lva_shared_prefix_attn(const lva_shared_prefix_params* p, const void*
                  int64_t(p->B) * p->steps, p->prefix_len,
                  p->q_token_stride, p->q_head_stride, p->k_token_stride, p->k_head_stride,
                  p->v_token_stride, p->v_head_stride, 0, 0, nullptr, nullptr, 0, p->scale,
-                 w.parts, part_o, part_lse, err};
+                 w.parts, part_o, part_lse, p->capacity > 0 ? 1 : 0, err};
     const cudaError_t e = launch_packed(a, stream, &why);
     if (e != cudaSuccess) return fail(LVA_ERR_CUDA, "shared_prefix: %s: %s", why, cudaGetErrorString(e));
   }

@@ -16,6 +16,11 @@
 // walked in order, raise the plane or the worker by one at each step, so plane + worker
 // numbers their slots without a table.
 //
+// With a prefix there are two kinds of work: the prefix parts (packed.cu) are bound by the
+// SMs' softmax rate, the caches by HBM, which half the SMs can saturate.  The caches' kernel
+// goes first on half the SMs, the prefix parts start beside it (a programmatic dependent
+// launch; neither reads what the other writes) and take over its SMs as it ends.
+//
 //   cache_attn_kernel  the last warp: TMA producer (K and V tiles of 64 keys in one ring, the
 //                      plane's Q rows in two slots); the others: mma.sync m16n8k16 on swizzled
 //                      tiles, in groups that take tiles in turn.  Keys are the M side (S^T =
@@ -259,6 +264,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
     *never = 0;
     mbar_fence_init();
   }
+  launch_dependents();                            // the prefix parts may start beside this kernel
   Walk walk(p, worker);
   __syncthreads();
 
@@ -431,32 +437,30 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
                 mx[nt][1] = fmax3(mx[nt][1], sf[i][nt][1], sf[i][nt][3]);
               }
             }
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(kFull, mx[nt][e], o));
-            // the reference moves only when a maximum outgrows it by 2^8 (weights stay in range)
-            float al[NT][2];
-            bool moved = false;
+            // The reference moves only when some maximum outgrows it by 2^8 (weights stay in
+            // range): one vote over the lanes' own maxima, and the rows' maxima only then.
+            bool out = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float old = m[nt][e];
-                if (mx[nt][e] > old + kRescaleThreshold || old == -INFINITY) m[nt][e] = fmaxf(old, mx[nt][e]);
-                al[nt][e] = m[nt][e] == old ? 1.f : ex2_approx(old - m[nt][e]);
-                moved |= m[nt][e] != old;
-              }
-            if (__any_sync(kFull, moved)) {
+              for (int e = 0; e < 2; ++e) out |= mx[nt][e] > m[nt][e] + kRescaleThreshold || m[nt][e] == -INFINITY;
+            if (__any_sync(kFull, out)) {
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(kFull, mx[nt][e], o));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  l[nt][e] *= al[nt][e];
+                  const float old = m[nt][e];
+                  if (mx[nt][e] > old + kRescaleThreshold || old == -INFINITY) m[nt][e] = fmaxf(old, mx[nt][e]);
+                  const float al = m[nt][e] == old ? 1.f : ex2_approx(old - m[nt][e]);
+                  l[nt][e] *= al;
 #pragma unroll
-                  for (int i = 0; i < D / 16; ++i) { of[i][nt][e] *= al[nt][e]; of[i][nt][e + 2] *= al[nt][e]; }
+                  for (int i = 0; i < D / 16; ++i) { of[i][nt][e] *= al; of[i][nt][e + 2] *= al; }
                 }
             }
 #pragma unroll
@@ -682,6 +686,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
     }
     const Parts x = parts_of(p, b, kvh, r, n, Runs(total, p.workers), before);
     const int t = r / p.group, head = kvh * p.group + (r - t * p.group);
+    wait_prerequisites();                          // the caller's lengths needed no wait
     constexpr int V = D / 32, AHEAD = 8;
     auto load = [&](int j, float (&v)[V]) {
       const float* src = (j < x.splits ? p.part_o : p.own_o) + x.at(p, j) * D + lane * V;
@@ -749,6 +754,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
   int before = 0;
   const int total = count_cost(p.lens, p.B, p.capacity, b, &before) * p.kv_heads;
   const Runs runs(total, p.workers);
+  wait_prerequisites();
   for (int r = warp; r < p.rows; r += kJoinThreads / 32) {
     const float lse = join_lse(p, parts_of(p, b, kvh, r, n, runs, before));
     if (lane == 0) row_lse[r] = lse == -INFINITY ? 0.f : lse;      // no weight: every score is -inf
@@ -827,9 +833,8 @@ cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream) {
   p.row_blocks = int((planes * rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
   p.chunks = a.weight != nullptr ? int((a.capacity + kChunk - 1) / kChunk) : 0;
   const unsigned blocks = unsigned(p.row_blocks + planes * p.chunks);
-  if (a.d == 128) join_kernel<128><<<blocks, kJoinThreads, 0, stream>>>(p);
-  else join_kernel<64><<<blocks, kJoinThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return a.d == 128 ? launch_dependent(join_kernel<128>, blocks, kJoinThreads, 0, stream, p)
+                    : launch_dependent(join_kernel<64>, blocks, kJoinThreads, 0, stream, p);
 }
 
 }  // namespace lva

@@ -48,6 +48,24 @@ inline int sm_count() {
   return n;
 }
 
+// Launches a kernel that may start before the one in front of it in the stream has ended (it
+// says when: launch_dependents, wait_prerequisites).
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t stream,
+                             const Args&... args) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 struct ReorderArgs {
   const void* src;
   void* dst;
@@ -195,6 +213,7 @@ struct PackedArgs {
   int splits;
   float* part_o;
   float* part_lse;
+  int beside;                // 1: launched to run beside the kernel before it in the stream
   int* err;
 };
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t stream, const char** why);

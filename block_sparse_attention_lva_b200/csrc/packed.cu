@@ -292,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.splits > 0) launch_dependents();          // the join gets ready
   const uint32_t tmem = *tmem_slot;
 
   // The next item of a role warp (every warp but the K producer): 1, or 0 after the last one,
@@ -780,8 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
       }
       ++nq;
       q_pending = true;
-    } else if (store) {
-      // No key for any row: O = 0 (this item has no Q buffer).
+    } else if (store && p.splits == 0) {
+      // No key for any row: O = 0 (this item has no Q buffer; a part of a prefix has keys).
       uint4* dst = reinterpret_cast<uint4*>(p.o + token * p.o_token + int64_t(head) * p.o_head + hf * DH);
 #pragma unroll 1
       for (int e = 0; e < DH / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
@@ -808,6 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  // Beside the caches' kernel: what waits for this kernel must find that one ended too.
+  if (p.splits > 0) wait_prerequisites();
 }
 
 template <int D>
@@ -855,6 +858,7 @@ cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why)
   p.err = a.err;
   const int64_t tiles = a.splits > 0 ? (a.total_q + tok - 1) / tok * a.splits : a.total_q / tok + a.num_seqs;
   const unsigned blocks = unsigned(tiles * a.kv_heads);
+  if (a.beside) return launch_dependent(packed_attn_kernel<D>, blocks, kThreads, C::SMEM_BYTES, stream, tq, tk, tv, to, p);
   packed_attn_kernel<D><<<blocks, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
   return cudaGetLastError();
 }

@@ -170,6 +170,14 @@ __device__ __forceinline__ int64_t clc_answer(uint32_t resp) {
   return got ? int64_t(x) : -1;
 }
 
+// ---------------------------------------------------------------- dependent launches
+// The next kernel of the stream, if launched as a programmatic dependent, may start once every
+// CTA of this one has said so (or ended).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Until the kernels this one was launched to depend on have ended and their writes are visible
+// (at once, in a kernel launched the ordinary way).
+__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- tcgen05
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
