@@ -518,7 +518,7 @@ static lva_status prefix_plan(const lva_shared_prefix_params* p, bool with_weigh
   const int64_t planes = int64_t(p->B) * p->kv_heads;
   const int64_t chunks = with_weight ? p->capacity / 512 + 1 : 0;
   if (planes >= most || planes * rows >= most || (p->capacity > 0 && planes >= most / p->capacity) ||
-      planes * rows / 4 + 1 + planes * chunks >= most)
+      planes * rows / 4 + 1 + planes * chunks >= most || planes * (p->capacity / 64 + 6) >= most)
     return fail(LVA_ERR_UNSUPPORTED, "shared_prefix: B * kv_heads * capacity and B * steps * q_heads must be < 2^31");
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   w->parts = prefix_parts(p);

@@ -73,13 +73,14 @@ __device__ __forceinline__ int live_len(const int32_t* lens, int b, int64_t capa
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile; }
 
 // A plane counts as its tiles and kSegment more: what a segment's start and end (its first
-// loads' latency, the join of its parts) cost beside its tiles.  Without it a worker with many
-// planes of a tile each took three times as long as the others (47 us instead of 16).
-constexpr int kSegment = 2;
+// loads' latency, the join of its parts) cost beside its tiles, 1.8 us against 0.36 us a tile
+// when latency counts.  Without it a worker with many planes of a tile each took three times as
+// long as the others (47 us instead of 16).
+constexpr int kSegment = 5;
 __device__ __forceinline__ int plane_cost(int tiles) { return tiles > 0 ? tiles + kSegment : 0; }
 
 // Cost of one head of all sequences, and of those before `stop` (whole warp).  All planes'
-// costs stay below 2^31: B * kv_heads * capacity / 64 and three times B * kv_heads do.
+// costs stay below 2^31: the call is refused when B * kv_heads * (capacity / 64 + 6) is not.
 __device__ __forceinline__ int count_cost(const int32_t* lens, int B, int64_t capacity, int stop, int* before) {
   const int lane = threadIdx.x & 31;
   int all = 0, part = 0;
@@ -687,7 +688,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
     const Parts x = parts_of(p, b, kvh, r, n, Runs(total, p.workers), before);
     const int t = r / p.group, head = kvh * p.group + (r - t * p.group);
     wait_prerequisites();                          // the caller's lengths needed no wait
-    constexpr int V = D / 32, AHEAD = 8;
+    constexpr int V = D / 32, AHEAD = 16;
     auto load = [&](int j, float (&v)[V]) {
       const float* src = (j < x.splits ? p.part_o : p.own_o) + x.at(p, j) * D + lane * V;
       if constexpr (V == 4) {

@@ -5,7 +5,7 @@ import random
 
 import pytest
 
-TILE, SEGMENT = 64, 2
+TILE, SEGMENT = 64, 5
 
 
 def tiles_of(n):
