@@ -103,7 +103,8 @@ SIGNATURES = {
     "lva_layer_step_host": (_c_int, [_vp, _vp, _vp, ctypes.POINTER(LvaLayerShape), ctypes.POINTER(LvaMaskParams),
                                      _vp, _c_int, _vp, _c_int, ctypes.POINTER(LvaHostStepBuffers), _c_int, _vp, _vp,
                                      _vp, ctypes.POINTER(ctypes.c_void_p)]),
-    "lva_packed_attn": (_c_int, [ctypes.POINTER(LvaPackedParams), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "lva_packed_workspace_bytes": (_c_i64, [ctypes.POINTER(LvaPackedParams)]),
+    "lva_packed_attn": (_c_int, [ctypes.POINTER(LvaPackedParams), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _vp]),
     "lva_shared_prefix_workspace_bytes": (_c_i64, [ctypes.POINTER(LvaSharedPrefixParams), _c_int]),
     "lva_shared_prefix_attn": (_c_int, [ctypes.POINTER(LvaSharedPrefixParams), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                         _vp, _vp, _c_i64, _vp]),
@@ -545,10 +546,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = True):
+def lva_packed_workspace_bytes(sequences: int, q_heads: int, kv_heads: int, d: int, total_q: int, total_k: int) -> int:
+    """Workspace bytes of ``lva_packed_attn`` for these sizes (0: none needed; -1: refused)."""
+    return lib.lva_packed_workspace_bytes(LvaPackedParams(sequences, q_heads, kv_heads, d, 1, 1.0, total_q, total_k))
+
+
+def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = True, workspace=None):
     """O, LSE of attention over packed sequences: q, o [total_q, Hq, d], k, v [total_k, Hkv, d]
     (bf16, rows contiguous, token and head strides free), lse [Hq, total_q] (fp32), cu_q and
-    cu_k [sequences + 1] (int32, device).  Causal: a sequence's last query sees all its keys."""
+    cu_k [sequences + 1] (int32, device).  Causal: a sequence's last query sees all its keys.
+    ``workspace``: uint8, ``lva_packed_workspace_bytes``; None takes what is needed from torch's
+    allocator (on the current stream, like any temporary)."""
     cur = _device_of(q, "q")
     if q.dim() != 3 or k.dim() != 3:
         _refuse("q and k must be [tokens, heads, d]")
@@ -562,9 +570,17 @@ def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = Tr
     n = p.num_seqs + 1
     if n < 1:
         _refuse("cu_q must have at least one entry")
+    ws, size = None, 0
+    if workspace is not None:
+        ws, size = _at_least(workspace, "workspace", torch.uint8, 0, cur), workspace.numel()
+    else:
+        size = lib.lva_packed_workspace_bytes(p)
+        if size > 0:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
     _check(lib.lva_packed_attn(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                _whole(lse, "lse", torch.float32, (hq, tq), cur), _whole(cu_q, "cu_q", torch.int32, (n,), cur),
-                               _whole(cu_k, "cu_k", torch.int32, (n,), cur), _raw_stream(cur)))
+                               _whole(cu_k, "cu_k", torch.int32, (n,), cur), ws, size, _raw_stream(cur)))
     return o, lse
 
 

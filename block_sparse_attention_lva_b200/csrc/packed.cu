@@ -31,6 +31,11 @@
 // memory.  The K producer decodes items and passes them to the other roles through a ring of
 // four in shared memory.
 //
+// Long key ranges with few tiles (p.part_blocks > 0): each tile's key blocks are cut into parts
+// of about part_blocks, the parts of all tiles form one list (counted from the lengths by every
+// CTA alike), and the CTAs take its items in turn.  A tile of one part is stored as usual, the
+// parts of the others are left like a prefix's and joined by packed_join_kernel.
+//
 // Pipeline and warp roles are those of the block-sparse kernel (attn.cu): three S buffers in
 // TMEM next to O, P over its own S, Q K^T and P V issued by two threads, K and V rings of
 // three 128-row TMA tiles, eight softmax warps with half a row per thread, exponentials
@@ -72,8 +77,11 @@ struct PackedParams {
   float* lse;                      // [Hq, total_q]
   int o_boxes;                     // 16 rows are whole tokens: O has a map with boxes of them
   int splits;                      // 0: packed; > 0: parts of the shared prefix
-  float* part_o;                   // [splits, kv_heads, total_q, group, D]
-  float* part_lse;                 // [splits, kv_heads, total_q, group], log2 units
+  int part_blocks, max_items;      // 0, or key blocks per part of a packed tile; items part_o holds
+  // Parts of a prefix [splits, kv_heads, total_q, group, D], or of packed tiles [items, 128, D],
+  // and their LSE in log2 units
+  float* part_o;
+  float* part_lse;
   int* err;
 };
 
@@ -81,7 +89,7 @@ struct PackedParams {
 // the key rows that start at k_row.
 struct Item {
   int kvh;
-  int split;
+  int64_t part_row0;       // where the tile's first row goes among the parts; -1: to O and LSE
   int tok0, q_end;         // first query token of the tile, end of its sequence
   int k_row, lk;           // first key row of the sequence, its keys
   int lim0;                // limit of the tile's first token, possibly below zero
@@ -153,30 +161,111 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int n, int tok, 
   }
 }
 
-// All item arithmetic is in 32 bits: tokens, tiles and the grid stay below 2^31.
+// A sequence's lengths; one whose entries fall or leave the buffers counts as empty.
+struct Sequence { int a, lq, ka, lk; };
+__device__ __forceinline__ Sequence sequence_at(const PackedParams& p, int s) {
+  const int a = __ldg(p.cu_q + s), b = __ldg(p.cu_q + s + 1);
+  const int ka = __ldg(p.cu_k + s), kb = __ldg(p.cu_k + s + 1);
+  const bool good = a >= 0 && a <= b && b <= p.total_q && ka >= 0 && ka <= kb && kb <= p.total_k;
+  return good ? Sequence{a, b - a, ka, kb - ka} : Sequence{0, 0, 0, 0};
+}
+// With part_blocks: tiles of a sequence, and parts that each of them is given (its longest
+// tile's; a causal tile of fewer blocks leaves the last ones empty).
+__device__ __forceinline__ int tiles_of(const PackedParams& p, int lq) { return int((uint32_t(lq) + p.tok - 1) / uint32_t(p.tok)); }
+__device__ __forceinline__ int parts_for(const PackedParams& p, int blocks) {
+  const int parts = int((uint32_t(blocks) + p.part_blocks - 1) / uint32_t(p.part_blocks));
+  return parts > 1 ? parts : 1;
+}
+__device__ __forceinline__ int blocks_of(int keys) { return int((uint32_t(keys) + BN - 1) / BN); }
+
+// Tile i0 .. i0 + tok - 1 of a sequence: its rows and key blocks.
+__device__ __forceinline__ void set_tile(const PackedParams& p, const Sequence& q, int i0, Item& w) {
+  const int last = (i0 + p.tok < q.lq ? i0 + p.tok : q.lq) - 1;
+  w.tok0 = q.a + i0;
+  w.q_end = q.a + q.lq;
+  w.k_row = q.ka;
+  w.lk = q.lk;
+  w.causal = p.causal;
+  w.lim0 = p.causal ? i0 + 1 + (q.lk - q.lq) : q.lk;
+  int lim_last = p.causal ? last + 1 + (q.lk - q.lq) : q.lk;
+  lim_last = lim_last < 0 ? 0 : lim_last;          // at most lk: last < lq
+  const int lim_first = w.lim0 < 0 ? 0 : w.lim0;
+  w.j0 = 0;
+  w.j1 = blocks_of(lim_last);
+  w.j_full = lim_first / BN;
+  w.part_row0 = -1;
+  w.live = 1;
+}
+// Part `part` of `parts` of an item's blocks.
+__device__ __forceinline__ void cut(Item& w, int part, int parts) {
+  const int full = w.j_full;
+  const uint32_t n = uint32_t(w.j1);
+  w.j0 = int(n * uint32_t(part) / uint32_t(parts));            // parts <= 64, blocks < 2^25
+  w.j1 = int(n * uint32_t(part + 1) / uint32_t(parts));
+  w.j_full = w.j1 < full ? w.j1 : full;
+  if (w.j_full < w.j0) w.j_full = w.j0;
+}
+
+// All item arithmetic is in 32 bits: tokens, tiles and the grid stay below 2^31.  live is 0
+// where there is nothing to do, -1 past the end of the list of parts.
 __device__ __forceinline__ Item item_at(const PackedParams& p, uint32_t bid) {
   Item w;
   w.live = 0;
-  w.split = 0;
-  const uint32_t rest = bid / uint32_t(p.kv_heads);
+  uint32_t rest = bid / uint32_t(p.kv_heads);
   w.kvh = int(bid - rest * p.kv_heads);
   if (p.splits > 0) {
     // Shared prefix: parts fastest after the head, so that the parts of a tile run together.
     const uint32_t tile = rest / uint32_t(p.splits);
-    w.split = int(rest - tile * p.splits);
+    const int split = int(rest - tile * p.splits);
     w.tok0 = int(tile * p.tok);
     w.q_end = int(p.total_q);
     w.k_row = 0;
     w.lk = int(p.total_k);
     w.lim0 = int(p.total_k);
     w.causal = 0;
-    const uint32_t nblk = uint32_t(p.total_k + BN - 1) / BN;     // parts <= 32, blocks < 2^25
-    w.j0 = int(nblk * w.split / uint32_t(p.splits));
-    w.j1 = int(nblk * (w.split + 1) / uint32_t(p.splits));
-    const int full = int(p.total_k / BN);
-    w.j_full = w.j1 < full ? w.j1 : full;
-    if (w.j_full < w.j0) w.j_full = w.j0;
+    w.j1 = blocks_of(int(p.total_k));
+    w.j_full = int(p.total_k / BN);
+    cut(w, split, p.splits);
+    w.part_row0 = ((int64_t(split) * p.kv_heads + w.kvh) * p.total_q + w.tok0) * p.group;
     w.live = w.tok0 < w.q_end ? 1 : 0;
+    return w;
+  }
+  if (p.part_blocks > 0) {
+    // The list: sequence by sequence, the last tile first, its parts in order, heads fastest.
+    const int lane = threadIdx.x & 31;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+      Sequence q{0, 0, 0, 0};
+      if (s0 + lane < p.num_seqs) q = sequence_at(p, s0 + lane);
+      const int parts = parts_for(p, blocks_of(q.lk));
+      const uint32_t own = uint32_t(tiles_of(p, q.lq)) * parts;
+      uint32_t sum = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, sum > rest);
+      if (past == 0) {
+        rest -= __shfl_sync(0xffffffffu, sum, 31);
+        continue;
+      }
+      const int l = __ffs(past) - 1;
+      const Sequence it{__shfl_sync(0xffffffffu, q.a, l), __shfl_sync(0xffffffffu, q.lq, l),
+                        __shfl_sync(0xffffffffu, q.ka, l), __shfl_sync(0xffffffffu, q.lk, l)};
+      const int given = __shfl_sync(0xffffffffu, parts, l);
+      const uint32_t in = rest - __shfl_sync(0xffffffffu, sum - own, l);
+      const uint32_t back = in / uint32_t(given);
+      const int part = int(in - back * given);
+      set_tile(p, it, int(tiles_of(p, it.lq) - 1 - back) * p.tok, w);
+      const int mine = parts_for(p, w.j1);
+      if (part >= mine || bid >= uint32_t(p.max_items)) w.live = 0;
+      else if (mine > 1) {
+        cut(w, part, mine);
+        w.part_row0 = int64_t(bid) * BM;
+      }
+      return w;
+    }
+    w.live = -1;
     return w;
   }
   // Packed: the last tiles of the last sequence first (a causal tile's work grows with its
@@ -184,29 +273,12 @@ __device__ __forceinline__ Item item_at(const PackedParams& p, uint32_t bid) {
   const uint32_t slot = uint32_t(p.total_q) / uint32_t(p.tok) + uint32_t(p.num_seqs) - 1u - rest;
   const int s = find_sequence(p.cu_q, p.num_seqs, p.tok, slot);
   if (s < 0) return w;
-  const int a = __ldg(p.cu_q + s), b = __ldg(p.cu_q + s + 1);
-  const int ka = __ldg(p.cu_k + s), kb = __ldg(p.cu_k + s + 1);
-  if (!(a >= 0 && a <= b && b <= p.total_q && ka >= 0 && ka <= kb && kb <= p.total_k)) return w;
-  const uint32_t first_slot = uint32_t(a) / uint32_t(p.tok) + uint32_t(s);
-  const int lq = b - a, lk = kb - ka;
+  const Sequence q = sequence_at(p, s);
+  const uint32_t first_slot = uint32_t(q.a) / uint32_t(p.tok) + uint32_t(s);
   // first token of the tile in its sequence; slots before the sequence's or past its tiles
-  const int64_t i0_wide = (int64_t(slot) - int64_t(first_slot)) * p.tok;
-  if (i0_wide < 0 || i0_wide >= lq) return w;
-  const int i0 = int(i0_wide);
-  const int last = (i0 + p.tok < lq ? i0 + p.tok : lq) - 1;
-  w.tok0 = a + i0;
-  w.q_end = b;
-  w.k_row = ka;
-  w.lk = lk;
-  w.causal = p.causal;
-  w.lim0 = p.causal ? i0 + 1 + (lk - lq) : lk;
-  int lim_last = p.causal ? last + 1 + (lk - lq) : lk;
-  lim_last = lim_last < 0 ? 0 : lim_last;          // at most lk: last < lq
-  const int lim_first = w.lim0 < 0 ? 0 : w.lim0;
-  w.j0 = 0;
-  w.j1 = int((uint32_t(lim_last) + BN - 1) / BN);
-  w.j_full = lim_first / BN;
-  w.live = 1;
+  const int64_t i0 = (int64_t(slot) - int64_t(first_slot)) * p.tok;
+  if (i0 < 0 || i0 >= q.lq) return w;
+  set_tile(p, q, int(i0), w);
   return w;
 }
 
@@ -289,10 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     mbar_fence_init();
   }
   if (warp == 1) { tmem_alloc(smem_u32(tmem_slot), kTmemCols); tmem_relinquish(); }
+  Item w0;                                        // the first item, found while the CTA is set up
+  if (warp == 0) w0 = item_at(p, blockIdx.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (p.splits > 0) launch_dependents();          // the join gets ready
+  if (p.part_o != nullptr) launch_dependents();   // the join gets ready
   const uint32_t tmem = *tmem_slot;
 
   // The next item of a role warp (every warp but the K producer): 1, or 0 after the last one,
@@ -319,8 +393,13 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     int64_t bid = blockIdx.x;                      // -1: no more items
     Item w;
     while (ok) {
-      if (bid >= 0) w = item_at(p, uint32_t(bid));
-      else w.live = 0;
+      w.live = -1;
+      if (bid == blockIdx.x) w = w0;
+      else if (bid >= 0) w = item_at(p, uint32_t(bid));
+      if (w.live < 0) {                              // no more items: the end mark
+        bid = -1;
+        w.live = 0;
+      }
       const int n = w.live ? w.j1 - w.j0 : 0;
       int64_t next = -1;
       if (w.live || bid < 0) {
@@ -342,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
         const int t_ask = n > kAhead ? n - kAhead : 0;
         bool asked = false;
         auto ask = [&] {
-          if (p.splits > 0) return;                // parts of a prefix are alike: one to a CTA
+          // parts of a prefix are alike: one to a CTA; parts of packed tiles are taken in turn
+          if (p.part_o != nullptr) return;
           mbar_arrive_expect_tx(bar_clc, 16);
           clc_try_cancel(resp, bar_clc);
           asked = true;
@@ -379,6 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
             ok = false;
           }
           ++answers;
+        } else if (ok && p.part_blocks > 0) {
+          next = bid + gridDim.x;
         }
       }
       bid = __shfl_sync(0xffffffffu, next, 0);
@@ -708,7 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     const bool none = !sees || l_row == 0.f;       // a NaN sum goes through as NaN
     const float inv_l = none ? 0.f : __fdividef(1.f, l_row);
     const int head = w.kvh * p.group + head_in;
-    const int64_t part_row = ((int64_t(w.split) * p.kv_heads + w.kvh) * p.total_q + token) * p.group + head_in;
+    const bool partial = w.part_row0 >= 0;
+    const int64_t part_row = w.part_row0 + row;
     // Rows go out through this item's Q buffer (its Q K^T is done), a warp's 16 rows in the tensor
     // maps' 128-byte swizzle, so staging meets no bank conflict.  When all 16 are rows of the
     // sequence and whole tokens (the group divides 16) one lane stores them as a box per 64
@@ -729,20 +812,35 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
           __syncwarp();
           if (lane == 0) mbar_arrive(bar_o_free);
         }
-        if (p.splits > 0) {
-          if (store) {
-            float* dst = p.part_o + part_row * D + hf * DH + q * 32;
+        if (partial) {
+          // 64 columns (32 of each half) of the warp's rows as floats, through the same 4 KB
+          // (d = 64: half of it a time): stores of whole 128-byte pieces.
+          constexpr int COLS = D == 128 ? 32 : 16;
 #pragma unroll
-            for (int e4 = 0; e4 < 8; ++e4) {
+          for (int c0 = 0; c0 < 32; c0 += COLS) {
+#pragma unroll
+            for (int u = 0; u < COLS / 4; ++u) {
               float4 f;
-              f.x = none ? 0.f : __uint_as_float(ov[4 * e4]) * inv_l;
-              f.y = none ? 0.f : __uint_as_float(ov[4 * e4 + 1]) * inv_l;
-              f.z = none ? 0.f : __uint_as_float(ov[4 * e4 + 2]) * inv_l;
-              f.w = none ? 0.f : __uint_as_float(ov[4 * e4 + 3]) * inv_l;
-              reinterpret_cast<float4*>(dst)[e4] = f;
+              f.x = none ? 0.f : __uint_as_float(ov[c0 + 4 * u]) * inv_l;
+              f.y = none ? 0.f : __uint_as_float(ov[c0 + 4 * u + 1]) * inv_l;
+              f.z = none ? 0.f : __uint_as_float(ov[c0 + 4 * u + 2]) * inv_l;
+              f.w = none ? 0.f : __uint_as_float(ov[c0 + 4 * u + 3]) * inv_l;
+              const int unit = hf * (COLS / 4) + u;
+              *reinterpret_cast<float4*>(smem + stage_off + r16 * (COLS * 8) + ((unit ^ (r16 & (COLS / 4 - 1))) << 4)) = f;
             }
+            __syncwarp();
+            constexpr int RU = COLS / 2, RPI = 32 / RU;          // units a row, rows an instruction
+            const int unit = lane % RU;
+            const int col = (unit / (RU / 2)) * DH + q * 32 + c0 + (unit % (RU / 2)) * 4;
+#pragma unroll
+            for (int r0 = 0; r0 < 16; r0 += RPI) {
+              const int r = r0 + lane / RU;
+              const int64_t at = __shfl_sync(0xffffffffu, store ? part_row : int64_t(-1), r);
+              const float4 f = *reinterpret_cast<const float4*>(smem + stage_off + r * (COLS * 8) + ((unit ^ (r & (COLS / 4 - 1))) << 4));
+              if (at >= 0) *reinterpret_cast<float4*>(p.part_o + at * D + col) = f;
+            }
+            __syncwarp();
           }
-          __syncwarp();
         } else {
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
@@ -756,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
           }
         }
       }
-      if (p.splits == 0) {
+      if (!partial) {
         if (__all_sync(0xffffffffu, store) && p.o_boxes) {
           fence_proxy_async_smem();
           __syncwarp();
@@ -778,10 +876,12 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
           }
           fence_proxy_async_smem();                // read before the buffer's next TMA write
         }
+      } else {
+        fence_proxy_async_smem();
       }
       ++nq;
       q_pending = true;
-    } else if (store && p.splits == 0) {
+    } else if (store && !partial) {
       // No key for any row: O = 0 (this item has no Q buffer; a part of a prefix has keys).
       uint4* dst = reinterpret_cast<uint4*>(p.o + token * p.o_token + int64_t(head) * p.o_head + hf * DH);
 #pragma unroll 1
@@ -789,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     }
     if (store && hf == 0) {
       const float lse2 = none ? -INFINITY : m_ref + __log2f(l_row);
-      if (p.splits > 0) p.part_lse[part_row] = lse2;
+      if (partial) p.part_lse[part_row] = lse2;
       else p.lse[int64_t(head) * p.total_q + token] = lse2 * kLn2;
     }
     __syncwarp();                                  // the next item's loads are the whole warp's
@@ -811,6 +911,111 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
   }
   // Beside the caches' kernel: what waits for this kernel must find that one ended too.
   if (p.splits > 0) wait_prerequisites();
+}
+
+// Joins the parts of packed tiles: a CTA per 32 rows of a (tile, head) of the unsplit
+// numbering, four rows a warp.
+//   LSE = log2 sum_j 2^(LSE_j),  O = sum_j 2^(LSE_j - LSE) O_j, in a fixed order.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 32;
+constexpr int kMaxParts = 64;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) packed_join_kernel(const PackedParams p) {
+  __shared__ float weight[kJoinRows][kMaxParts + 1];
+  __shared__ float row_lse[kJoinRows];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t tile = blockIdx.x / (BM / kJoinRows);
+  const int first = int(blockIdx.x % (BM / kJoinRows)) * kJoinRows;
+  const uint32_t slot = tile / uint32_t(p.kv_heads);
+  const int kvh = int(tile - slot * p.kv_heads);
+  // Every warp finds the tile and its place in the list of parts by itself.  A CTA with nothing
+  // to join waits all the same: this kernel's end stands for the one before it.
+  Item w;
+  w.live = 0;
+  int parts = 1;
+  uint32_t item0 = 0;
+  const int s = find_sequence(p.cu_q, p.num_seqs, p.tok, slot);
+  if (s >= 0) {
+    const Sequence q = sequence_at(p, s);
+    const int64_t i0 = (int64_t(slot) - int64_t(uint32_t(q.a) / uint32_t(p.tok) + uint32_t(s))) * p.tok;
+    if (i0 >= 0 && i0 < q.lq) {
+      set_tile(p, q, int(i0), w);
+      parts = parts_for(p, w.j1);
+      uint32_t before = 0;
+      for (int x = lane; x < s; x += 32) {
+        const Sequence y = sequence_at(p, x);
+        before += uint32_t(tiles_of(p, y.lq)) * parts_for(p, blocks_of(y.lk));
+      }
+      before = __reduce_add_sync(0xffffffffu, before);
+      const uint32_t back = uint32_t(tiles_of(p, q.lq)) - 1u - uint32_t(i0) / uint32_t(p.tok);
+      item0 = (before + back * parts_for(p, blocks_of(q.lk))) * p.kv_heads + kvh;
+    }
+  }
+  wait_prerequisites();
+  // (the bound on the items fails only for lengths that were refused)
+  if (w.live <= 0 || parts == 1 || item0 + uint32_t(parts - 1) * p.kv_heads >= uint32_t(p.max_items)) return;
+  const int rows = (w.q_end - w.tok0 < p.tok ? w.q_end - w.tok0 : p.tok) * p.group - first;   // from `first` on
+  if (rows <= 0) return;
+  const int64_t row0 = int64_t(item0) * BM + first, step = int64_t(p.kv_heads) * BM;
+  // A warp's four rows: lanes over the parts for the weights, then over the columns.
+  constexpr int V = D / 32, ROWS = kJoinRows / (kJoinThreads / 32);
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = warp * ROWS + i;
+    if (r >= rows) break;
+    const float x = lane < parts ? p.part_lse[row0 + lane * step + r] : -INFINITY;
+    const float y = lane + 32 < parts ? p.part_lse[row0 + (lane + 32) * step + r] : -INFINITY;
+    float top = fmaxf(x, y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float use = top == -INFINITY ? 0.f : top;
+    float sum = ex2_approx(x - use) + ex2_approx(y - use);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float lse = sum == 0.f ? -INFINITY : use + __log2f(sum);
+    const float base = lse == -INFINITY ? 0.f : lse;
+    weight[r][lane] = ex2_approx(x - base);
+    weight[r][lane + 32] = ex2_approx(y - base);
+    if (lane == 0) row_lse[r] = lse;
+  }
+  __syncwarp();
+  float acc[ROWS][V] = {};
+#pragma unroll 4
+  for (int j = 0; j < parts; ++j) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int r = warp * ROWS + i;
+      if (r < rows) {
+        const float a = weight[r][j];
+        const float* src = p.part_o + (row0 + j * step + r) * D + lane * V;
+        float v[V];
+        if constexpr (V == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(src);
+          v[0] = f.x; v[1] = f.y;
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[i][e] = fmaf(a, v[e], acc[i][e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int r = warp * ROWS + i;
+    if (r < rows) {
+      const int tok_in = (first + r) / p.group, head = kvh * p.group + (first + r) - tok_in * p.group;
+      const int64_t token = int64_t(w.tok0) + tok_in;
+      __nv_bfloat16* dst = p.o + token * p.o_token + int64_t(head) * p.o_head + lane * V;
+      if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[i][0], acc[i][1]), pack_bf16x2(acc[i][2], acc[i][3]));
+      else
+        *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[i][0], acc[i][1]);
+      if (lane == 0) p.lse[int64_t(head) * p.total_q + token] = row_lse[r] * kLn2;
+    }
+  }
 }
 
 template <int D>
@@ -853,14 +1058,20 @@ cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why)
   p.lse = a.lse;
   p.o_boxes = boxes ? 1 : 0;
   p.splits = a.splits;
+  p.part_blocks = a.part_blocks;
+  p.max_items = a.max_items;
   p.part_o = a.part_o;
   p.part_lse = a.part_lse;
   p.err = a.err;
   const int64_t tiles = a.splits > 0 ? (a.total_q + tok - 1) / tok * a.splits : a.total_q / tok + a.num_seqs;
   const unsigned blocks = unsigned(tiles * a.kv_heads);
   if (a.beside) return launch_dependent(packed_attn_kernel<D>, blocks, kThreads, C::SMEM_BYTES, stream, tq, tk, tv, to, p);
-  packed_attn_kernel<D><<<blocks, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
-  return cudaGetLastError();
+  const unsigned grid = a.part_blocks > 0 && a.max_items < 148 ? unsigned(a.max_items) : a.part_blocks > 0 ? 148u : blocks;
+  packed_attn_kernel<D><<<grid, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.part_blocks == 0) return e;
+  *why = "join launch";
+  return launch_dependent(packed_join_kernel<D>, blocks * (BM / kJoinRows), kJoinThreads, 0, stream, p);
 }
 
 }  // namespace

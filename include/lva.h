@@ -490,6 +490,12 @@ lva_status lva_layer_step_host(const void* qkv_host, void* o_host, float* lse_ho
  * or leave the buffers is skipped and reported through lva_device_error as
  * LVA_ERR_INVALID_ARG (detail = the sequence).
  *
+ * workspace: NULL, or device, 16-byte aligned, at least lva_packed_workspace_bytes bytes: with
+ * one, the long key ranges of few query tokens are cut into parts that fill the GPU and are
+ * joined in a second launch.  Its contents have no meaning between calls; calls (and captured
+ * graphs) that may run at the same time need one each.  Without it every call is right, and
+ * slower where few tokens meet many keys.
+ *
  * Keys outside a sequence never matter, whatever memory holds there.  Inside a sequence, a
  * value that is not finite at a causally unseen key can reach the rows of the same tile of
  * 128 rows (its weight there is zero, and zero times infinity is not).
@@ -497,7 +503,7 @@ lva_status lva_layer_step_host(const void* qkv_host, void* o_host, float* lse_ho
  * Errors: LVA_ERR_INVALID_ARG for null or misaligned pointers, bad strides or sizes, q_heads
  * not a multiple of kv_heads, or a scale that is not positive and finite; LVA_ERR_UNSUPPORTED
  * for d other than 64 and 128, more than 128 query heads per key/value head, totals of 2^31
- * tokens, or more tiles than one launch covers.  num_seqs == 0 or total_q == 0 is a no-op.
+ * tokens, or more tiles than one launch covers; LVA_ERR_CAPACITY for a small workspace.  num_seqs == 0 or total_q == 0 is a no-op.
  */
 typedef struct {
   int num_seqs;
@@ -512,9 +518,13 @@ typedef struct {
   int64_t o_token_stride, o_head_stride;
 } lva_packed_params;
 
+/* Workspace bytes for params (0 when there is nothing to gain from one; -1 for bad params). */
+int64_t lva_packed_workspace_bytes(const lva_packed_params* params);
+
 lva_status lva_packed_attn(const lva_packed_params* params, const void* q, const void* k,
                            const void* v, void* o, float* lse, const int32_t* cu_q,
-                           const int32_t* cu_k, cudaStream_t stream);
+                           const int32_t* cu_k, void* workspace, int64_t workspace_bytes,
+                           cudaStream_t stream);
 
 /*
  * lva_shared_prefix_attn -- attention of a step's tokens over a key prefix that the whole

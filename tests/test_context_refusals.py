@@ -12,14 +12,14 @@ from block_sparse_attention_lva_b200 import _binding as lb
 OK, INVALID, UNSUPPORTED, CAPACITY = 0, 1, 2, 3
 
 
-def packed(q=16, k=16, v=16, o=16, lse=4, cu_q=4, cu_k=4, **kw):
+def packed(q=16, k=16, v=16, o=16, lse=4, cu_q=4, cu_k=4, ws=None, ws_bytes=0, **kw):
     p = dict(num_seqs=2, q_heads=4, kv_heads=2, d=64, causal=1, scale=0.125, total_q=100, total_k=100,
              q_token_stride=256, q_head_stride=64, k_token_stride=128, k_head_stride=64, v_token_stride=128,
              v_head_stride=64, o_token_stride=256, o_head_stride=64)
     p.update(kw)
     vp = ctypes.c_void_p
     return lb.lib.lva_packed_attn(ctypes.byref(lb.LvaPackedParams(**p)), vp(q), vp(k), vp(v), vp(o), vp(lse), vp(cu_q),
-                                  vp(cu_k), None)
+                                  vp(cu_k), vp(ws), ws_bytes, None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -38,6 +38,7 @@ def packed(q=16, k=16, v=16, o=16, lse=4, cu_q=4, cu_k=4, **kw):
     (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(o=None), INVALID), (dict(lse=None), INVALID), (dict(cu_q=None), INVALID),
     (dict(cu_k=None), INVALID),
     (dict(num_seqs=0, q=None), OK), (dict(total_q=0, q=None), OK),
+    (dict(ws=8), INVALID), (dict(ws=256, ws_bytes=1000, total_k=5000), CAPACITY),
 ])
 def test_packed(kw, status):
     assert packed(**kw) == status
@@ -45,7 +46,20 @@ def test_packed(kw, status):
 
 
 def test_packed_null_params():
-    assert lb.lib.lva_packed_attn(None, *[ctypes.c_void_p(16)] * 7, None) == INVALID
+    assert lb.lib.lva_packed_attn(None, *[ctypes.c_void_p(16)] * 8, 0, None) == INVALID
+
+
+def test_packed_workspace():
+    size = lva.lva_packed_workspace_bytes
+    assert size(2, 4, 2, 64, 100, 100) == 0                   # one key block: nothing to cut
+    assert size(1, 4, 2, 128, 100000, 100000) == 0            # tiles enough
+    assert size(0, 4, 2, 64, 0, 100000) == 0
+    assert 0 < size(1, 4, 2, 64, 1, 8000) < size(1, 4, 2, 128, 1, 8000)
+    # never past 2,048 parts of 128 rows
+    for args in ((6, 40, 8, 128, 962, 15269), (1, 128, 1, 64, 300, 1 << 20), (500, 1, 1, 128, 500, 1 << 24), (1, 2, 2, 128, 1, 1 << 30)):
+        assert 0 <= size(*args) <= 2048 * 128 * (128 * 4 + 4)
+    assert size(2, 3, 2, 64, 100, 100) == -1 and size(2, 4, 2, 64, -1, 100) == -1
+    assert lb.lib.lva_packed_workspace_bytes(None) == -1
 
 
 def _bf(*shape):

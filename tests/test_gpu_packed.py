@@ -87,6 +87,58 @@ def test_group_sizes(hq, hk):
     compare(q, k, v, o, lse, cu(ql), cu(kl), 0.125, True)
 
 
+# Few tokens against long key ranges: the tiles are cut into parts along the keys
+LONG = {
+    "one_token": ([1], [8000]),
+    "tokens": ([64, 1, 3], [5000, 900, 131]),
+    "short_and_long": ([130, 0, 300, 1], [130, 700, 3333, 6]),
+    "continued_prompt": ([700], [2700]),
+    "more_queries": ([700, 20], [600, 2000]),
+}
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("hq,hk,d", [(1, 1, 128), (10, 2, 64), (8, 2, 128)])
+@pytest.mark.parametrize("name", list(LONG))
+def test_parts_along_the_keys(name, hq, hk, d, causal):
+    import block_sparse_attention_lva_b200 as lva
+    dev = require_gpu()
+    ql, kl = LONG[name]
+    assert lva.lva_packed_workspace_bytes(len(ql), hq, hk, d, sum(ql), sum(kl) + 70) > 0
+    g = torch.Generator().manual_seed(sum(name.encode()) + hq + d)
+    q, k, v = make(g, sum(ql), sum(kl) + 70, hq, hk, d, dev)
+    k[sum(kl):] = float("nan")
+    v[sum(kl):] = float("nan")
+    o, lse = run(lva, q, k, v, cu(ql), cu(kl), d ** -0.5, causal)
+    assert lva.lva_device_error() == (0, 0)
+    compare(q, k, v, o, lse, cu(ql), cu(kl), float(np.float32(d ** -0.5)), causal)
+    # the caller's own workspace (its contents do not matter), and none at all through the C call
+    ws = torch.full((lva.lva_packed_workspace_bytes(len(ql), hq, hk, d, *[x.shape[0] for x in (q, k)]),), 0xff, dtype=torch.uint8, device=dev)
+    o2, lse2 = torch.zeros_like(o), torch.zeros_like(lse)
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=dev) for x in (cu(ql), cu(kl)))
+    lva.lva_packed_attn(q, k, v, o2, lse2, cq, ck, d ** -0.5, causal=causal, workspace=ws)
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(o2), bits(o)) and np.array_equal(bits(lse2), bits(lse))
+
+
+def test_parts_with_refused_lengths():
+    # a list that falls may count more tiles than the totals allow: nothing is written past the
+    # workspace (its end is checked), the sequences are reported
+    import block_sparse_attention_lva_b200 as lva
+    dev = require_gpu()
+    q, k, v = make(torch.Generator().manual_seed(3), 128, 4000, 1, 1, 64, dev)
+    cq = torch.tensor([0, 128] * 20, dtype=torch.int32, device=dev)
+    ck = torch.tensor([0, 4000] * 20, dtype=torch.int32, device=dev)
+    n = lva.lva_packed_workspace_bytes(39, 1, 1, 64, 128, 4000)
+    assert n > 0
+    ws = torch.full((n + 4096,), 7, dtype=torch.uint8, device=dev)
+    o, lse = torch.zeros_like(q), torch.zeros((1, 128), device=dev)
+    lva.lva_packed_attn(q, k, v, o, lse, cq, ck, 0.1, workspace=ws)
+    torch.cuda.synchronize()
+    assert lva.lva_device_error()[0] == 1
+    assert (ws[n:] == 7).all()
+
+
 def test_many_sequences():
     # more sequences than one round of the warp's search covers, many of them empty
     import block_sparse_attention_lva_b200 as lva
