@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -54,24 +55,11 @@ class LvaHostStepBuffers(ctypes.Structure):
                 ("nnz", ctypes.c_void_p), ("events", ctypes.POINTER(ctypes.c_void_p)), ("num_events", ctypes.c_int)]
 
 
-class LvaPackedParams(ctypes.Structure):
-    """Mirror of ``lva_packed_params``."""
-    _fields_ = [("num_seqs", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("d", ctypes.c_int),
-                ("causal", ctypes.c_int), ("scale", ctypes.c_float), ("total_q", ctypes.c_int64),
-                ("total_k", ctypes.c_int64), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
-                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
-                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
-                ("o_token_stride", ctypes.c_int64), ("o_head_stride", ctypes.c_int64)]
-
-
-class LvaSharedPrefixParams(ctypes.Structure):
-    """Mirror of ``lva_shared_prefix_params``."""
-    _fields_ = [("B", ctypes.c_int), ("steps", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
-                ("d", ctypes.c_int), ("scale", ctypes.c_float), ("prefix_len", ctypes.c_int64),
-                ("capacity", ctypes.c_int64), ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
-                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
-                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
-                ("o_token_stride", ctypes.c_int64), ("o_head_stride", ctypes.c_int64)]
+# The parameter structs of the context calls, packed in their C layout and passed as bytes:
+# lva_packed_params and lva_shared_prefix_params (native sizes and alignment).
+_PACKED = struct.Struct("@5if10q")       # num_seqs, q_heads, kv_heads, d, causal, scale, totals, strides of q, k, v, o
+_PREFIX = struct.Struct("@5if10q")       # B, steps, q_heads, kv_heads, d, scale, prefix_len, capacity, strides of q, k, v, o
+_params = ctypes.c_char_p
 
 
 SIGNATURES = {
@@ -103,10 +91,10 @@ SIGNATURES = {
     "lva_layer_step_host": (_c_int, [_vp, _vp, _vp, ctypes.POINTER(LvaLayerShape), ctypes.POINTER(LvaMaskParams),
                                      _vp, _c_int, _vp, _c_int, ctypes.POINTER(LvaHostStepBuffers), _c_int, _vp, _vp,
                                      _vp, ctypes.POINTER(ctypes.c_void_p)]),
-    "lva_packed_workspace_bytes": (_c_i64, [ctypes.POINTER(LvaPackedParams)]),
-    "lva_packed_attn": (_c_int, [ctypes.POINTER(LvaPackedParams), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _vp]),
-    "lva_shared_prefix_workspace_bytes": (_c_i64, [ctypes.POINTER(LvaSharedPrefixParams), _c_int]),
-    "lva_shared_prefix_attn": (_c_int, [ctypes.POINTER(LvaSharedPrefixParams), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+    "lva_packed_workspace_bytes": (_c_i64, [_params]),
+    "lva_packed_attn": (_c_int, [_params, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _vp]),
+    "lva_shared_prefix_workspace_bytes": (_c_i64, [_params, _c_int]),
+    "lva_shared_prefix_attn": (_c_int, [_params, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                         _vp, _vp, _c_i64, _vp]),
     "lva_append_cache": (_c_int, [_vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int,
                                   _c_int, _c_i64, _c_int, _vp]),
@@ -464,75 +452,72 @@ def lva_layer_step_host(qkv_host, o_host, lse_host, shape: LvaLayerShape, params
     return done.value
 
 
-# The context calls below are short, and a step of a rollout makes several of them: their
-# checks build no message and convert no argument unless one fails, and read the stream
-# without making a Stream object.
+# The context calls below are short, and a step of a rollout makes several of them: a tensor's
+# checks are a few comparisons, what is wrong with one is found out only when they fail, and the
+# stream is read without making a Stream object.
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _refuse(msg: str):
     raise ValueError(msg)
 
 
-def _on_device(t, name: str, dtype, cur: int):
+def _explain(t, name: str, dtype, shape, cur: int):
+    """Raises what is wrong with a tensor that is not ``dtype`` [``shape``] on device ``cur``."""
     if t is None or not t.is_cuda:
         _refuse(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         _refuse(f"{name} must be {dtype}, got {t.dtype}")
     if t.get_device() != cur:
         _refuse(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{cur}")
+    if tuple(t.shape) != tuple(shape):
+        _refuse(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _refuse(f"{name} must be contiguous")
 
 
 def _heads_view(t, name: str, shape, cur: int):
     """Checks a bf16 CUDA tensor [tokens, heads, d] on the current device whose rows are
     contiguous (token and head strides are free: slices of a fused projection serve as they
     are); returns (token stride, head stride)."""
-    _on_device(t, name, torch.bfloat16, cur)
-    if t.shape != shape:
-        _refuse(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t is None or t.dtype is not _BF16 or t.get_device() != cur or t.shape != shape:
+        _explain(t, name, _BF16, shape, cur)
     st, sh, se = t.stride()
-    return _strides(name, st, sh, se, *shape)
-
-
-def _strides(name: str, st: int, sh: int, se: int, tokens: int, heads: int, d: int):
     if se != 1:
         _refuse(f"{name} must be contiguous in its last dimension")
-    if tokens <= 1:      # the stride of a dimension of one element is never walked, whatever the view says
-        st = d if heads <= 1 else heads * max(sh, d)
+    if shape[0] <= 1:    # the stride of a dimension of one element is never walked, whatever the view says
+        st = shape[2] if shape[1] <= 1 else shape[1] * max(sh, shape[2])
     return st, sh
 
 
 def _steps_view(t, name: str, shape, cur: int):
     """``_heads_view`` of a [B, steps, heads, d] tensor whose tokens have one stride."""
-    _on_device(t, name, torch.bfloat16, cur)
-    if t.shape != shape:
-        _refuse(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t is None or t.dtype is not _BF16 or t.get_device() != cur or t.shape != shape:
+        _explain(t, name, _BF16, shape, cur)
     B, steps, heads, d = shape
     sb, st, sh, se = t.stride()
+    if se != 1:
+        _refuse(f"{name} must be contiguous in its last dimension")
     if steps == 1:       # a batch of single tokens has the batch's own stride
         st = sb
     elif B > 1 and sb != steps * st:
         _refuse(f"{name}: the tokens of a batch must have one stride")
-    return _strides(name, st, sh, se, B * steps, heads, d)
+    if B * steps <= 1:
+        st = d if heads <= 1 else heads * max(sh, d)
+    return st, sh
 
 
 def _whole(t, name: str, dtype, shape, cur: int):
     """Address of a contiguous CUDA tensor of exactly this shape on the current device."""
-    _on_device(t, name, dtype, cur)
-    if t.shape != shape:
-        _refuse(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        _refuse(f"{name} must be contiguous")
+    if t is None or t.dtype is not dtype or t.get_device() != cur or t.shape != shape or not t.is_contiguous():
+        _explain(t, name, dtype, shape, cur)
     return t.data_ptr()
 
 
-def _at_least(t, name: str, dtype, numel: int, cur: int):
-    """Address of a contiguous CUDA tensor with ``numel`` elements or more."""
-    _on_device(t, name, dtype, cur)
-    if not t.is_contiguous():
-        _refuse(f"{name} must be contiguous")
-    if t.numel() < numel:
-        _refuse(f"{name} has {t.numel()} elements, needs {numel}")
-    return t.data_ptr()
+def _bytes_of(t, name: str, cur: int):
+    """Address and size of a contiguous uint8 CUDA tensor on the current device."""
+    if t is None or t.dtype is not _U8 or t.get_device() != cur or not t.is_contiguous():
+        _explain(t, name, _U8, () if t is None else t.shape, cur)
+    return t.data_ptr(), t.numel()
 
 
 def _device_of(t, name: str) -> int:
@@ -548,7 +533,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def lva_packed_workspace_bytes(sequences: int, q_heads: int, kv_heads: int, d: int, total_q: int, total_k: int) -> int:
     """Workspace bytes of ``lva_packed_attn`` for these sizes (0: none needed; -1: refused)."""
-    return lib.lva_packed_workspace_bytes(LvaPackedParams(sequences, q_heads, kv_heads, d, 1, 1.0, total_q, total_k))
+    return lib.lva_packed_workspace_bytes(_PACKED.pack(sequences, q_heads, kv_heads, d, 1, 1.0, total_q, total_k, *[0] * 8))
 
 
 def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = True, workspace=None):
@@ -564,30 +549,30 @@ def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = Tr
     tq, hq, d = qshape
     tk, hk = k.shape[:2]
     kshape = (tk, hk, d)
-    p = LvaPackedParams(cu_q.numel() - 1, hq, hk, d, 1 if causal else 0, scale, tq, tk,
-                        *_heads_view(q, "q", qshape, cur), *_heads_view(k, "k", kshape, cur),
-                        *_heads_view(v, "v", kshape, cur), *_heads_view(o, "o", qshape, cur))
-    n = p.num_seqs + 1
+    n = cu_q.numel()
     if n < 1:
         _refuse("cu_q must have at least one entry")
+    p = _PACKED.pack(n - 1, hq, hk, d, 1 if causal else 0, scale, tq, tk,
+                     *_heads_view(q, "q", qshape, cur), *_heads_view(k, "k", kshape, cur),
+                     *_heads_view(v, "v", kshape, cur), *_heads_view(o, "o", qshape, cur))
     ws, size = None, 0
     if workspace is not None:
-        ws, size = _at_least(workspace, "workspace", torch.uint8, 0, cur), workspace.numel()
+        ws, size = _bytes_of(workspace, "workspace", cur)
     else:
         size = lib.lva_packed_workspace_bytes(p)
         if size > 0:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(size, dtype=_U8, device=q.device)
             ws = workspace.data_ptr()
     _check(lib.lva_packed_attn(p, q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                               _whole(lse, "lse", torch.float32, (hq, tq), cur), _whole(cu_q, "cu_q", torch.int32, (n,), cur),
-                               _whole(cu_k, "cu_k", torch.int32, (n,), cur), ws, size, _raw_stream(cur)))
+                               _whole(lse, "lse", _F32, (hq, tq), cur), _whole(cu_q, "cu_q", _I32, (n,), cur),
+                               _whole(cu_k, "cu_k", _I32, (n,), cur), ws, size, _raw_stream(cur)))
     return o, lse
 
 
 def lva_shared_prefix_workspace_bytes(B: int, steps: int, q_heads: int, kv_heads: int, d: int, prefix_len: int,
                                       capacity: int, with_weight: bool = False) -> int:
     """Workspace bytes of ``lva_shared_prefix_attn`` for these sizes (-1 for sizes it refuses)."""
-    p = LvaSharedPrefixParams(B, steps, q_heads, kv_heads, d, 1.0, prefix_len, capacity)
+    p = _PREFIX.pack(B, steps, q_heads, kv_heads, d, 1.0, prefix_len, capacity, *[0] * 8)
     return lib.lva_shared_prefix_workspace_bytes(p, 1 if with_weight else 0)
 
 
@@ -610,14 +595,14 @@ def lva_shared_prefix_attn(q, prefix_k, prefix_v, k_cache, v_cache, lens, o, lse
         pshape = (lp, hk, d)
         ks, vs = _heads_view(prefix_k, "prefix_k", pshape, cur), _heads_view(prefix_v, "prefix_v", pshape, cur)
         pk, pv = prefix_k.data_ptr(), prefix_v.data_ptr()
-    p = LvaSharedPrefixParams(B, steps, hq, hk, d, scale, lp, cap, *_steps_view(q, "q", qshape, cur), *ks, *vs,
-                              *_steps_view(o, "o", qshape, cur))
+    p = _PREFIX.pack(B, steps, hq, hk, d, scale, lp, cap, *_steps_view(q, "q", qshape, cur), *ks, *vs,
+                     *_steps_view(o, "o", qshape, cur))
     _check(lib.lva_shared_prefix_attn(
-        p, q.data_ptr(), pk, pv, _whole(k_cache, "k_cache", torch.bfloat16, cshape, cur),
-        _whole(v_cache, "v_cache", torch.bfloat16, cshape, cur), _whole(lens, "lens", torch.int32, (B,), cur), o.data_ptr(),
-        _whole(lse, "lse", torch.float32, (B, hq, steps), cur),
-        None if weight is None else _whole(weight, "weight", torch.float32, cshape[:3], cur),
-        _at_least(workspace, "workspace", torch.uint8, 0, cur), workspace.numel(), _raw_stream(cur)))
+        p, q.data_ptr(), pk, pv, _whole(k_cache, "k_cache", _BF16, cshape, cur),
+        _whole(v_cache, "v_cache", _BF16, cshape, cur), _whole(lens, "lens", _I32, (B,), cur), o.data_ptr(),
+        _whole(lse, "lse", _F32, (B, hq, steps), cur),
+        None if weight is None else _whole(weight, "weight", _F32, cshape[:3], cur),
+        *_bytes_of(workspace, "workspace", cur), _raw_stream(cur)))
     return o, lse
 
 
@@ -634,10 +619,10 @@ def lva_append_cache(k_new, v_new, k_cache, v_cache, weight, lens, lens_out):
     cshape = (B, hk, cap, d)
     ks, vs = _steps_view(k_new, "k_new", shape, cur), _steps_view(v_new, "v_new", shape, cur)
     _check(lib.lva_append_cache(
-        k_new.data_ptr(), v_new.data_ptr(), *ks, *vs, _whole(k_cache, "k_cache", torch.bfloat16, cshape, cur),
-        _whole(v_cache, "v_cache", torch.bfloat16, cshape, cur),
-        None if weight is None else _whole(weight, "weight", torch.float32, cshape[:3], cur),
-        _whole(lens, "lens", torch.int32, (B,), cur), _whole(lens_out, "lens_out", torch.int32, (B,), cur),
+        k_new.data_ptr(), v_new.data_ptr(), *ks, *vs, _whole(k_cache, "k_cache", _BF16, cshape, cur),
+        _whole(v_cache, "v_cache", _BF16, cshape, cur),
+        None if weight is None else _whole(weight, "weight", _F32, cshape[:3], cur),
+        _whole(lens, "lens", _I32, (B,), cur), _whole(lens_out, "lens_out", _I32, (B,), cur),
         B, steps, hk, cap, d, _raw_stream(cur)))
     return lens_out
 
@@ -653,13 +638,12 @@ def lva_evict_cache(k_cache, v_cache, weight, lens, k_out, v_out, weight_out, le
     shape = k_cache.shape
     B, hk, cap, d = shape
     wshape = (B, hk, cap)
-    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
     _check(lib.lva_evict_cache(
-        _whole(k_cache, "k_cache", bf16, shape, cur), _whole(v_cache, "v_cache", bf16, shape, cur),
-        _whole(weight, "weight", f32, wshape, cur), _whole(lens, "lens", i32, (B,), cur),
-        _whole(k_out, "k_out", bf16, shape, cur), _whole(v_out, "v_out", bf16, shape, cur),
-        _whole(weight_out, "weight_out", f32, wshape, cur), _whole(lens_out, "lens_out", i32, (B,), cur),
-        _whole(kept, "kept", i32, (B, hk, budget), cur), B, hk, cap, d, budget, sinks, recent, _raw_stream(cur)))
+        _whole(k_cache, "k_cache", _BF16, shape, cur), _whole(v_cache, "v_cache", _BF16, shape, cur),
+        _whole(weight, "weight", _F32, wshape, cur), _whole(lens, "lens", _I32, (B,), cur),
+        _whole(k_out, "k_out", _BF16, shape, cur), _whole(v_out, "v_out", _BF16, shape, cur),
+        _whole(weight_out, "weight_out", _F32, wshape, cur), _whole(lens_out, "lens_out", _I32, (B,), cur),
+        _whole(kept, "kept", _I32, (B, hk, budget), cur), B, hk, cap, d, budget, sinks, recent, _raw_stream(cur)))
     return k_out, v_out, weight_out, lens_out, kept
 
 

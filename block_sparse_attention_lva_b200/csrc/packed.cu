@@ -61,8 +61,11 @@ constexpr float kRescaleThreshold = 8.0f;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
 
-// One pair of exponentials in four on the FMA pipe (as in the block-sparse kernel).
-__device__ __forceinline__ constexpr bool poly_pair(int e) { return e % 4 == 3; }
+// One pair of exponentials in eight on the FMA pipe.  Under a load that holds the card at its
+// power limit the MUFU's exponentials cost less than the polynomial's steps: one causal
+// sequence of 16,379 tokens took 790 us with one pair in eight, 797 with one in sixteen, 799
+// with none, 822 with one in four, 842 and 872 with three in eight and one in three.
+__device__ __forceinline__ constexpr bool poly_pair(int e) { return e % 8 == 7; }
 
 struct PackedParams {
   int num_seqs;
@@ -208,12 +211,13 @@ __device__ __forceinline__ void cut(Item& w, int part, int parts) {
 
 // All item arithmetic is in 32 bits: tokens, tiles and the grid stay below 2^31.  live is 0
 // where there is nothing to do, -1 past the end of the list of parts.
+template <bool PARTS>
 __device__ __forceinline__ Item item_at(const PackedParams& p, uint32_t bid) {
   Item w;
   w.live = 0;
   uint32_t rest = bid / uint32_t(p.kv_heads);
   w.kvh = int(bid - rest * p.kv_heads);
-  if (p.splits > 0) {
+  if (PARTS && p.splits > 0) {
     // Shared prefix: parts fastest after the head, so that the parts of a tile run together.
     const uint32_t tile = rest / uint32_t(p.splits);
     const int split = int(rest - tile * p.splits);
@@ -230,7 +234,7 @@ __device__ __forceinline__ Item item_at(const PackedParams& p, uint32_t bid) {
     w.live = w.tok0 < w.q_end ? 1 : 0;
     return w;
   }
-  if (p.part_blocks > 0) {
+  if (PARTS && p.part_blocks > 0) {
     // The list: sequence by sequence, the last tile first, its parts in order, heads fastest.
     const int lane = threadIdx.x & 31;
     for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
@@ -296,7 +300,9 @@ __device__ __noinline__ void rescale_o(uint32_t taddr, float alpha) {
   }
 }
 
-template <int D>
+// PARTS: the call may leave parts to a join (a shared prefix, or tiles cut along the keys); the
+// form without them keeps that code out of the loops (it cost them 10 %).
+template <int D, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const PackedParams p) {
@@ -309,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
   }
   // The first CTA checks both length lists: a list that falls or leaves its buffer is
   // reported, and the sequences it spoils are skipped where they are met.
-  if (blockIdx.x == 0 && p.splits == 0) {
+  if (blockIdx.x == 0 && (!PARTS || p.splits == 0)) {
     for (int s = threadIdx.x; s < p.num_seqs; s += kThreads) {
       const int64_t a = __ldg(p.cu_q + s), b = __ldg(p.cu_q + s + 1);
       const int64_t ka = __ldg(p.cu_k + s), kb = __ldg(p.cu_k + s + 1);
@@ -362,11 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
   }
   if (warp == 1) { tmem_alloc(smem_u32(tmem_slot), kTmemCols); tmem_relinquish(); }
   Item w0;                                        // the first item, found while the CTA is set up
-  if (warp == 0) w0 = item_at(p, blockIdx.x);
+  if (warp == 0) w0 = item_at<PARTS>(p, blockIdx.x);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (p.part_o != nullptr) launch_dependents();   // the join gets ready
+  if (PARTS) launch_dependents();                 // the join gets ready
   const uint32_t tmem = *tmem_slot;
 
   // The next item of a role warp (every warp but the K producer): 1, or 0 after the last one,
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     while (ok) {
       w.live = -1;
       if (bid == blockIdx.x) w = w0;
-      else if (bid >= 0) w = item_at(p, uint32_t(bid));
+      else if (bid >= 0) w = item_at<PARTS>(p, uint32_t(bid));
       if (w.live < 0) {                              // no more items: the end mark
         bid = -1;
         w.live = 0;
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
         bool asked = false;
         auto ask = [&] {
           // parts of a prefix are alike: one to a CTA; parts of packed tiles are taken in turn
-          if (p.part_o != nullptr) return;
+          if (PARTS) return;
           mbar_arrive_expect_tx(bar_clc, 16);
           clc_try_cancel(resp, bar_clc);
           asked = true;
@@ -459,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
             ok = false;
           }
           ++answers;
-        } else if (ok && p.part_blocks > 0) {
+        } else if (PARTS && ok && p.part_blocks > 0) {
           next = bid + gridDim.x;
         }
       }
@@ -790,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     const bool none = !sees || l_row == 0.f;       // a NaN sum goes through as NaN
     const float inv_l = none ? 0.f : __fdividef(1.f, l_row);
     const int head = w.kvh * p.group + head_in;
-    const bool partial = w.part_row0 >= 0;
+    const bool partial = PARTS && w.part_row0 >= 0;
     const int64_t part_row = w.part_row0 + row;
     // Rows go out through this item's Q buffer (its Q K^T is done), a warp's 16 rows in the tensor
     // maps' 128-byte swizzle, so staging meets no bank conflict.  When all 16 are rows of the
@@ -832,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
             constexpr int RU = COLS / 2, RPI = 32 / RU;          // units a row, rows an instruction
             const int unit = lane % RU;
             const int col = (unit / (RU / 2)) * DH + q * 32 + c0 + (unit % (RU / 2)) * 4;
-#pragma unroll
+#pragma unroll 1
             for (int r0 = 0; r0 < 16; r0 += RPI) {
               const int r = r0 + lane / RU;
               const int64_t at = __shfl_sync(0xffffffffu, store ? part_row : int64_t(-1), r);
@@ -910,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     tmem_dealloc(tmem, kTmemCols);
   }
   // Beside the caches' kernel: what waits for this kernel must find that one ended too.
-  if (p.splits > 0) wait_prerequisites();
+  if (PARTS && p.splits > 0) wait_prerequisites();
 }
 
 // Joins the parts of packed tiles: a CTA per 32 rows of a (tile, head) of the unsplit
@@ -1018,7 +1024,7 @@ __global__ void __launch_bounds__(kJoinThreads) packed_join_kernel(const PackedP
   }
 }
 
-template <int D>
+template <int D, bool PARTS>
 cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why) {
   using C = Cfg<D>;
   const int group = a.q_heads / a.kv_heads, tok = BM / group;
@@ -1038,7 +1044,7 @@ cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why)
   if (!boxes) to = tq;                             // not used
   static DeviceFlags attr_set = {};
   cudaError_t e = once_per_device(attr_set, [] {
-    return cudaFuncSetAttribute(packed_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    return cudaFuncSetAttribute(packed_attn_kernel<D, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   });
   if (e != cudaSuccess) { *why = "cudaFuncSetAttribute(max dynamic smem) failed"; return e; }
   PackedParams p;
@@ -1065,11 +1071,11 @@ cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why)
   p.err = a.err;
   const int64_t tiles = a.splits > 0 ? (a.total_q + tok - 1) / tok * a.splits : a.total_q / tok + a.num_seqs;
   const unsigned blocks = unsigned(tiles * a.kv_heads);
-  if (a.beside) return launch_dependent(packed_attn_kernel<D>, blocks, kThreads, C::SMEM_BYTES, stream, tq, tk, tv, to, p);
+  if (a.beside) return launch_dependent(packed_attn_kernel<D, PARTS>, blocks, kThreads, C::SMEM_BYTES, stream, tq, tk, tv, to, p);
   const unsigned grid = a.part_blocks > 0 && a.max_items < 148 ? unsigned(a.max_items) : a.part_blocks > 0 ? 148u : blocks;
-  packed_attn_kernel<D><<<grid, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
+  packed_attn_kernel<D, PARTS><<<grid, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || a.part_blocks == 0) return e;
+  if (e != cudaSuccess || !PARTS || a.part_blocks == 0) return e;
   *why = "join launch";
   return launch_dependent(packed_join_kernel<D>, blocks * (BM / kJoinRows), kJoinThreads, 0, stream, p);
 }
@@ -1077,8 +1083,8 @@ cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why)
 }  // namespace
 
 cudaError_t launch_packed(const PackedArgs& a, cudaStream_t stream, const char** why) {
-  if (a.d == 128) return launch_d<128>(a, stream, why);
-  if (a.d == 64) return launch_d<64>(a, stream, why);
+  if (a.d == 128) return a.part_o ? launch_d<128, true>(a, stream, why) : launch_d<128, false>(a, stream, why);
+  if (a.d == 64) return a.part_o ? launch_d<64, true>(a, stream, why) : launch_d<64, false>(a, stream, why);
   *why = "unsupported d";
   return cudaErrorInvalidValue;
 }

@@ -12,13 +12,18 @@ from block_sparse_attention_lva_b200 import _binding as lb
 OK, INVALID, UNSUPPORTED, CAPACITY = 0, 1, 2, 3
 
 
+def packed_bytes(p):
+    return lb._PACKED.pack(*[p[k] for k in ("num_seqs", "q_heads", "kv_heads", "d", "causal", "scale", "total_q", "total_k")],
+                           *[p[f"{t}_{s}_stride"] for t in "qkvo" for s in ("token", "head")])
+
+
 def packed(q=16, k=16, v=16, o=16, lse=4, cu_q=4, cu_k=4, ws=None, ws_bytes=0, **kw):
     p = dict(num_seqs=2, q_heads=4, kv_heads=2, d=64, causal=1, scale=0.125, total_q=100, total_k=100,
              q_token_stride=256, q_head_stride=64, k_token_stride=128, k_head_stride=64, v_token_stride=128,
              v_head_stride=64, o_token_stride=256, o_head_stride=64)
     p.update(kw)
     vp = ctypes.c_void_p
-    return lb.lib.lva_packed_attn(ctypes.byref(lb.LvaPackedParams(**p)), vp(q), vp(k), vp(v), vp(o), vp(lse), vp(cu_q),
+    return lb.lib.lva_packed_attn(packed_bytes(p), vp(q), vp(k), vp(v), vp(o), vp(lse), vp(cu_q),
                                   vp(cu_k), vp(ws), ws_bytes, None)
 
 
@@ -43,6 +48,12 @@ def packed(q=16, k=16, v=16, o=16, lse=4, cu_q=4, cu_k=4, ws=None, ws_bytes=0, *
 def test_packed(kw, status):
     assert packed(**kw) == status
     assert (lb.lib.lva_last_error_message() == b"") == (status == OK)
+
+
+def test_parameter_layouts():
+    # the packed bytes are the C structs (include/lva.h): five ints, a float, ten 64-bit integers
+    assert lb._PACKED.size == lb._PREFIX.size == 104
+    assert lb._PACKED.pack(1, 2, 3, 4, 5, 1.0, *range(10))[24:32] == (0).to_bytes(8, "little")
 
 
 def test_packed_null_params():
@@ -77,12 +88,13 @@ def prefix_params(**kw):
              q_head_stride=64, k_token_stride=128, k_head_stride=64, v_token_stride=128, v_head_stride=64,
              o_token_stride=256, o_head_stride=64)
     p.update(kw)
-    return lb.LvaSharedPrefixParams(**p)
+    return lb._PREFIX.pack(*[p[k] for k in ("B", "steps", "q_heads", "kv_heads", "d", "scale", "prefix_len", "capacity")],
+                           *[p[f"{t}_{s}_stride"] for t in "qkvo" for s in ("token", "head")])
 
 
 def prefix(q=16, pk=16, pv=16, kc=16, vc=16, lens=4, o=16, lse=4, weight=None, ws=256, ws_bytes=1 << 40, **kw):
     vp = ctypes.c_void_p
-    return lb.lib.lva_shared_prefix_attn(ctypes.byref(prefix_params(**kw)), vp(q), vp(pk), vp(pv), vp(kc), vp(vc), vp(lens),
+    return lb.lib.lva_shared_prefix_attn(prefix_params(**kw), vp(q), vp(pk), vp(pv), vp(kc), vp(vc), vp(lens),
                                          vp(o), vp(lse), vp(weight), vp(ws), ws_bytes, None)
 
 
@@ -110,7 +122,7 @@ def test_shared_prefix(kw, status):
 
 
 def test_shared_prefix_workspace():
-    size = lambda w=0, **kw: lb.lib.lva_shared_prefix_workspace_bytes(ctypes.byref(prefix_params(**kw)), w)
+    size = lambda w=0, **kw: lb.lib.lva_shared_prefix_workspace_bytes(prefix_params(**kw), w)
     for kw, _ in SIZES:
         assert size(**kw) == -1, kw
     assert lb.lib.lva_shared_prefix_workspace_bytes(None, 0) == -1
