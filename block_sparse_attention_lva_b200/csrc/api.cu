@@ -440,13 +440,14 @@ static lva_status check_heads(const char* fn, int q_heads, int kv_heads, int d, 
 }
 
 // Parts of packed tiles, when there are tiles for less than half the SMs (an upper bound from the
-// totals; the lengths are on the device) and at least 20 key blocks: 64 tokens of 40 heads
-// against 8,000 keys, 24 tiles, take 41 us in parts and 62 us whole, but 128 tiles of 32 blocks
-// 47 us and 45.  A part is at least six blocks (its start and end cost that much), at least half
-// an SM's even share of the estimated work, and as long as the bound of 2,048 parts (135 MB at
-// d = 128) wants.
+// totals; the lengths are on the device) and at least 20 key blocks.  The kernel cuts the tiles
+// into at most 148 parts, one per SM: 64 tokens of 40 heads against 8,000 keys, 24 tiles, take
+// 31 us so, 37 in up to twice as many parts, 60 whole; 512 tokens of 8 heads against 16,384
+// keys 47, 52 and 112.  With tiles for most SMs the parts' start, end and join cost what they
+// gain: 128 tiles of 32 blocks took 45 us whole and 48 to 61 cut, 264 of 125 blocks 301 and
+// 307 to 337.
 struct PackedPlan {
-  int part_blocks, max_items;        // 0: no parts
+  int spare, max_items;              // 0: no parts
   int64_t part_o, part_lse, bytes;   // byte offsets in the workspace
 };
 
@@ -455,17 +456,9 @@ static PackedPlan packed_plan(const lva_packed_params* p) {
   const int tok = 128 / (p->q_heads / p->kv_heads);
   const int64_t tiles = (p->total_q / tok + p->num_seqs) * p->kv_heads;
   const int64_t blocks = (p->total_k + 127) / 128;
-  if (p->num_seqs == 0 || p->total_q == 0 || tiles >= 74) return w;
-  const int64_t room = 2048 / tiles < 64 ? 2048 / tiles : 64;
-  if (room < 2 || blocks < 20) return w;
-  const int64_t per_seq = (blocks + p->num_seqs - 1) / p->num_seqs;
-  int64_t size = (tiles * per_seq + 295) / 296;
-  if (size < (blocks + room - 1) / room) size = (blocks + room - 1) / room;
-  if (size < 6) size = 6;
-  const int64_t parts = (blocks + size - 1) / size;
-  if (parts < 2) return w;
-  w.part_blocks = int(size);
-  w.max_items = int(tiles * parts);
+  if (p->num_seqs == 0 || p->total_q == 0 || tiles >= 74 || blocks < 20) return w;
+  w.max_items = 148;
+  w.spare = w.max_items - int(tiles);
   w.part_lse = int64_t(w.max_items) * 128 * p->d * 4;
   w.bytes = w.part_lse + int64_t(w.max_items) * 128 * 4;
   return w;
@@ -519,9 +512,9 @@ lva_status lva_packed_attn(const lva_packed_params* p, const void* q, const void
   PackedArgs a{q, k, v, o, lse, p->num_seqs, p->q_heads, p->kv_heads, p->d, p->total_q, p->total_k,
                p->q_token_stride, p->q_head_stride, p->k_token_stride, p->k_head_stride,
                p->v_token_stride, p->v_head_stride, p->o_token_stride, p->o_head_stride,
-               cu_q, cu_k, p->causal != 0, p->scale, 0, w.part_blocks, w.max_items,
-               w.part_blocks > 0 ? reinterpret_cast<float*>(ws + w.part_o) : nullptr,
-               w.part_blocks > 0 ? reinterpret_cast<float*>(ws + w.part_lse) : nullptr, 0, err};
+               cu_q, cu_k, p->causal != 0, p->scale, 0, w.spare, w.max_items,
+               w.spare > 0 ? reinterpret_cast<float*>(ws + w.part_o) : nullptr,
+               w.spare > 0 ? reinterpret_cast<float*>(ws + w.part_lse) : nullptr, 0, err};
   const char* why = "launch";
   const cudaError_t e = launch_packed(a, stream, &why);
   if (e != cudaSuccess) return fail(LVA_ERR_CUDA, "packed: %s: %s", why, cudaGetErrorString(e));

@@ -211,7 +211,7 @@ struct PackedArgs {
   int causal;
   float scale;
   int splits;
-  int part_blocks, max_items;  // packed: 0, or key blocks per part of a tile and the parts' room
+  int spare, max_items;      // packed: 0, or parts there may be beyond one per tile, and items part_o holds
   float* part_o;
   float* part_lse;
   int beside;                // 1: launched to run beside the kernel before it in the stream

@@ -31,10 +31,10 @@
 // memory.  The K producer decodes items and passes them to the other roles through a ring of
 // four in shared memory.
 //
-// Long key ranges with few tiles (p.part_blocks > 0): each tile's key blocks are cut into parts
-// of about part_blocks, the parts of all tiles form one list (counted from the lengths by every
-// CTA alike), and the CTAs take its items in turn.  A tile of one part is stored as usual, the
-// parts of the others are left like a prefix's and joined by packed_join_kernel.
+// Long key ranges with few tiles (p.spare > 0): tiles are cut along their key blocks into parts
+// of about an equal share, at most one per SM in all, counted from the lengths by every CTA
+// alike.  A tile of one part is stored as usual, the parts of the others are left like a
+// prefix's and joined by packed_join_kernel.
 //
 // Pipeline and warp roles are those of the block-sparse kernel (attn.cu): three S buffers in
 // TMEM next to O, P over its own S, Q K^T and P V issued by two threads, rings of three K
@@ -80,7 +80,7 @@ struct PackedParams {
   float* lse;                      // [Hq, total_q]
   int o_boxes;                     // 16 rows are whole tokens: O has a map with boxes of them
   int splits;                      // 0: packed; > 0: parts of the shared prefix
-  int part_blocks, max_items;      // 0, or key blocks per part of a packed tile; items part_o holds
+  int spare, max_items;            // packed in parts: parts there may be beyond one per tile (0: none), items part_o holds
   // Parts of a prefix [splits, kv_heads, total_q, group, D], or of packed tiles [items, 128, D],
   // and their LSE in log2 units
   float* part_o;
@@ -172,14 +172,40 @@ __device__ __forceinline__ Sequence sequence_at(const PackedParams& p, int s) {
   const bool good = a >= 0 && a <= b && b <= p.total_q && ka >= 0 && ka <= kb && kb <= p.total_k;
   return good ? Sequence{a, b - a, ka, kb - ka} : Sequence{0, 0, 0, 0};
 }
-// With part_blocks: tiles of a sequence, and parts that each of them is given (its longest
-// tile's; a causal tile of fewer blocks leaves the last ones empty).
+__device__ __forceinline__ int blocks_of(int keys) { return int((uint32_t(keys) + BN - 1) / BN); }
 __device__ __forceinline__ int tiles_of(const PackedParams& p, int lq) { return int((uint32_t(lq) + p.tok - 1) / uint32_t(p.tok)); }
-__device__ __forceinline__ int parts_for(const PackedParams& p, int blocks) {
-  const int parts = int((uint32_t(blocks) + p.part_blocks - 1) / uint32_t(p.part_blocks));
+
+// Key blocks per part of a packed tile (whole warp; the same in every CTA of a call): all tiles'
+// blocks, as of their sequences' last tiles, divided by `spare`, so that the parts are at most
+// `spare` more than the tiles; at least kLeastPart, which a part's start and end cost, and
+// not more than kMostParts parts.
+constexpr int kLeastPart = 6;
+constexpr int kMostParts = 64;
+__device__ __forceinline__ int part_size(const PackedParams& p) {
+  unsigned long long work = 0;
+  int longest = 0;
+  for (int s = threadIdx.x & 31; s < p.num_seqs; s += 32) {
+    const Sequence q = sequence_at(p, s);
+    const int blocks = blocks_of(q.lk);
+    if (q.lq > 0) {
+      work += uint64_t(tiles_of(p, q.lq)) * uint32_t(blocks);
+      longest = blocks > longest ? blocks : longest;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  work = (work * uint32_t(p.kv_heads) + uint32_t(p.spare) - 1) / uint32_t(p.spare);
+  const int even = work < (1u << 24) ? int(work) : 1 << 24, least = (longest + kMostParts - 1) / kMostParts;
+  const int size = even > least ? even : least;
+  return size > kLeastPart ? size : kLeastPart;
+}
+// Parts that each tile of a sequence is given in the list (its longest tile's; a causal tile of
+// fewer blocks leaves the last ones empty).
+__device__ __forceinline__ int parts_for(int blocks, int size) {
+  const int parts = int((uint32_t(blocks) + uint32_t(size) - 1) / uint32_t(size));
   return parts > 1 ? parts : 1;
 }
-__device__ __forceinline__ int blocks_of(int keys) { return int((uint32_t(keys) + BN - 1) / BN); }
 
 // Tile i0 .. i0 + tok - 1 of a sequence: its rows and key blocks.
 __device__ __forceinline__ void set_tile(const PackedParams& p, const Sequence& q, int i0, Item& w) {
@@ -210,9 +236,9 @@ __device__ __forceinline__ void cut(Item& w, int part, int parts) {
 }
 
 // All item arithmetic is in 32 bits: tokens, tiles and the grid stay below 2^31.  live is 0
-// where there is nothing to do, -1 past the end of the list of parts.
+// where there is nothing to do; `size` is used with p.spare.
 template <bool PARTS>
-__device__ __forceinline__ Item item_at(const PackedParams& p, uint32_t bid) {
+__device__ __forceinline__ Item item_at(const PackedParams& p, uint32_t bid, int size) {
   Item w;
   w.live = 0;
   uint32_t rest = bid / uint32_t(p.kv_heads);
@@ -234,13 +260,13 @@ __device__ __forceinline__ Item item_at(const PackedParams& p, uint32_t bid) {
     w.live = w.tok0 < w.q_end ? 1 : 0;
     return w;
   }
-  if (PARTS && p.part_blocks > 0) {
+  if (PARTS && p.spare > 0) {
     // The list: sequence by sequence, the last tile first, its parts in order, heads fastest.
     const int lane = threadIdx.x & 31;
     for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
       Sequence q{0, 0, 0, 0};
       if (s0 + lane < p.num_seqs) q = sequence_at(p, s0 + lane);
-      const int parts = parts_for(p, blocks_of(q.lk));
+      const int parts = parts_for(blocks_of(q.lk), size);
       const uint32_t own = uint32_t(tiles_of(p, q.lq)) * parts;
       uint32_t sum = own;
 #pragma unroll
@@ -261,15 +287,14 @@ __device__ __forceinline__ Item item_at(const PackedParams& p, uint32_t bid) {
       const uint32_t back = in / uint32_t(given);
       const int part = int(in - back * given);
       set_tile(p, it, int(tiles_of(p, it.lq) - 1 - back) * p.tok, w);
-      const int mine = parts_for(p, w.j1);
-      if (part >= mine || bid >= uint32_t(p.max_items)) w.live = 0;
+      const int mine = parts_for(w.j1, size);
+      if (part >= mine) w.live = 0;
       else if (mine > 1) {
         cut(w, part, mine);
         w.part_row0 = int64_t(bid) * BM;
       }
       return w;
     }
-    w.live = -1;
     return w;
   }
   // Packed: the last tiles of the last sequence first (a causal tile's work grows with its
@@ -368,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
   }
   if (warp == 1) { tmem_alloc(smem_u32(tmem_slot), kTmemCols); tmem_relinquish(); }
   Item w0;                                        // the first item, found while the CTA is set up
-  if (warp == 0) w0 = item_at<PARTS>(p, blockIdx.x);
+  if (warp == 0) w0 = item_at<PARTS>(p, blockIdx.x, PARTS && p.spare > 0 ? part_size(p) : 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -401,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
     while (ok) {
       w.live = -1;
       if (bid == blockIdx.x) w = w0;
-      else if (bid >= 0) w = item_at<PARTS>(p, uint32_t(bid));
+      else if (!PARTS && bid >= 0) w = item_at<PARTS>(p, uint32_t(bid), 0);
       if (w.live < 0) {                              // no more items: the end mark
         bid = -1;
         w.live = 0;
@@ -427,9 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
         const int t_ask = n > kAhead ? n - kAhead : 0;
         bool asked = false;
         auto ask = [&] {
-          // Parts of packed tiles are taken in turn; parts of a prefix are one to a CTA: SMs become
-          // free for them bit by bit, as the caches' kernel ends, and CTAs that started first
-          // would take two (a batch of 32: 48 us instead of 36).
+          // Parts are one to a CTA.  Those of packed tiles all run at once; a prefix's find SMs
+          // bit by bit, as the caches' kernel ends, and CTAs that started first would take two
+          // (a batch of 32: 48 us instead of 36).
           if (PARTS) return;
           mbar_arrive_expect_tx(bar_clc, 16);
           clc_try_cancel(resp, bar_clc);
@@ -467,8 +492,6 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
             ok = false;
           }
           ++answers;
-        } else if (PARTS && ok && p.part_blocks > 0) {
-          next = bid + gridDim.x;
         }
       }
       bid = __shfl_sync(0xffffffffu, next, 0);
@@ -926,11 +949,10 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
 //   LSE = log2 sum_j 2^(LSE_j),  O = sum_j 2^(LSE_j - LSE) O_j, in a fixed order.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 32;
-constexpr int kMaxParts = 64;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) packed_join_kernel(const PackedParams p) {
-  __shared__ float weight[kJoinRows][kMaxParts + 1];
+  __shared__ float weight[kJoinRows][kMostParts + 1];
   __shared__ float row_lse[kJoinRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t tile = blockIdx.x / (BM / kJoinRows);
@@ -943,21 +965,22 @@ __global__ void __launch_bounds__(kJoinThreads) packed_join_kernel(const PackedP
   w.live = 0;
   int parts = 1;
   uint32_t item0 = 0;
+  const int size = part_size(p);
   const int s = find_sequence(p.cu_q, p.num_seqs, p.tok, slot);
   if (s >= 0) {
     const Sequence q = sequence_at(p, s);
     const int64_t i0 = (int64_t(slot) - int64_t(uint32_t(q.a) / uint32_t(p.tok) + uint32_t(s))) * p.tok;
     if (i0 >= 0 && i0 < q.lq) {
       set_tile(p, q, int(i0), w);
-      parts = parts_for(p, w.j1);
+      parts = parts_for(w.j1, size);
       uint32_t before = 0;
       for (int x = lane; x < s; x += 32) {
         const Sequence y = sequence_at(p, x);
-        before += uint32_t(tiles_of(p, y.lq)) * parts_for(p, blocks_of(y.lk));
+        before += uint32_t(tiles_of(p, y.lq)) * parts_for(blocks_of(y.lk), size);
       }
       before = __reduce_add_sync(0xffffffffu, before);
       const uint32_t back = uint32_t(tiles_of(p, q.lq)) - 1u - uint32_t(i0) / uint32_t(p.tok);
-      item0 = (before + back * parts_for(p, blocks_of(q.lk))) * p.kv_heads + kvh;
+      item0 = (before + back * parts_for(blocks_of(q.lk), size)) * p.kv_heads + kvh;
     }
   }
   wait_prerequisites();
@@ -1066,7 +1089,7 @@ cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why)
   p.lse = a.lse;
   p.o_boxes = boxes ? 1 : 0;
   p.splits = a.splits;
-  p.part_blocks = a.part_blocks;
+  p.spare = a.spare;
   p.max_items = a.max_items;
   p.part_o = a.part_o;
   p.part_lse = a.part_lse;
@@ -1074,10 +1097,10 @@ cudaError_t launch_d(const PackedArgs& a, cudaStream_t stream, const char** why)
   const int64_t tiles = a.splits > 0 ? (a.total_q + tok - 1) / tok * a.splits : a.total_q / tok + a.num_seqs;
   const unsigned blocks = unsigned(tiles * a.kv_heads);
   if (a.beside) return launch_dependent(packed_attn_kernel<D, PARTS>, blocks, kThreads, C::SMEM_BYTES, stream, tq, tk, tv, to, p);
-  const unsigned grid = a.part_blocks > 0 && a.max_items < 148 ? unsigned(a.max_items) : a.part_blocks > 0 ? 148u : blocks;
+  const unsigned grid = a.spare > 0 ? unsigned(a.max_items) : blocks;
   packed_attn_kernel<D, PARTS><<<grid, kThreads, C::SMEM_BYTES, stream>>>(tq, tk, tv, to, p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || !PARTS || a.part_blocks == 0) return e;
+  if (e != cudaSuccess || !PARTS || a.spare == 0) return e;
   *why = "join launch";
   return launch_dependent(packed_join_kernel<D>, blocks * (BM / kJoinRows), kJoinThreads, 0, stream, p);
 }

@@ -488,11 +488,12 @@ lva_status lva_layer_step_host(const void* qkv_host, void* o_host, float* lse_ho
  * [0, total_q] and [0, total_k]: tokens before cu_q[0] or after cu_q[num_seqs] are in no
  * sequence, and their rows of o and lse are left as they were.  A sequence whose entries fall
  * or leave the buffers is skipped and reported through lva_device_error as
- * LVA_ERR_INVALID_ARG (detail = the sequence).
+ * LVA_ERR_INVALID_ARG (detail = the sequence); beside one whose entries fall, others can be
+ * skipped too.
  *
  * workspace: NULL, or device, 16-byte aligned, at least lva_packed_workspace_bytes bytes: with
- * one, the long key ranges of few query tokens are cut into parts that fill the GPU and are
- * joined in a second launch.  Its contents have no meaning between calls; calls (and captured
+ * one, the long key ranges of few query tokens are cut into parts that fill the GPU (at most
+ * 148 of 128 rows: 9.8 MB) and are joined in a second launch.  Its contents have no meaning between calls; calls (and captured
  * graphs) that may run at the same time need one each.  Without it every call is right, and
  * slower where few tokens meet many keys.
  *
@@ -503,7 +504,8 @@ lva_status lva_layer_step_host(const void* qkv_host, void* o_host, float* lse_ho
  * Errors: LVA_ERR_INVALID_ARG for null or misaligned pointers, bad strides or sizes, q_heads
  * not a multiple of kv_heads, or a scale that is not positive and finite; LVA_ERR_UNSUPPORTED
  * for d other than 64 and 128, more than 128 query heads per key/value head, totals of 2^31
- * tokens, or more tiles than one launch covers; LVA_ERR_CAPACITY for a small workspace.  num_seqs == 0 or total_q == 0 is a no-op.
+ * tokens, or more tiles than one launch covers; LVA_ERR_CAPACITY for a small workspace.
+ * num_seqs == 0 or total_q == 0 is a no-op.
  */
 typedef struct {
   int num_seqs;

@@ -66,9 +66,9 @@ def test_packed_workspace():
     assert size(1, 4, 2, 128, 100000, 100000) == 0            # tiles enough
     assert size(0, 4, 2, 64, 0, 100000) == 0
     assert 0 < size(1, 4, 2, 64, 1, 8000) < size(1, 4, 2, 128, 1, 8000)
-    # never past 2,048 parts of 128 rows
+    # never past 148 parts of 128 rows
     for args in ((6, 40, 8, 128, 962, 15269), (1, 128, 1, 64, 300, 1 << 20), (500, 1, 1, 128, 500, 1 << 24), (1, 2, 2, 128, 1, 1 << 30)):
-        assert 0 <= size(*args) <= 2048 * 128 * (128 * 4 + 4)
+        assert 0 <= size(*args) <= 148 * 128 * (128 * 4 + 4)
     assert size(2, 3, 2, 64, 100, 100) == -1 and size(2, 4, 2, 64, -1, 100) == -1
     assert lb.lib.lva_packed_workspace_bytes(None) == -1
 

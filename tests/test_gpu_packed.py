@@ -93,6 +93,8 @@ LONG = {
     "tokens": ([64, 1, 3], [5000, 900, 131]),
     "short_and_long": ([130, 0, 300, 1], [130, 700, 3333, 6]),
     "continued_prompt": ([700], [2700]),
+    "one_long_of_many": ([1] * 30, [50] * 29 + [9000]),
+    "uneven": ([40, 1, 0, 3], [2000, 9001, 700, 5]),
     "more_queries": ([700, 20], [600, 2000]),
 }
 
