@@ -521,29 +521,51 @@ lva_status lva_packed_attn(const lva_packed_params* p, const void* q, const void
   return ok();
 }
 
-// Parts of the prefix.  In block times (128 rows by 128 keys), with c = items * parts CTAs on
-// 148 SMs, the pass takes about blocks / parts when c <= 148, or items * blocks / 148 and half a
-// part of tail when there are more, and in either case 3 for a part's start and end; a part's
-// rows cost the join their bytes, written and read (about 7.2 MB a block time).
-static int prefix_parts(const lva_shared_prefix_params* p) {
-  if (p->prefix_len == 0) return 0;
-  const int tok = 128 / (p->q_heads / p->kv_heads);
+// Parts of the prefix and workers of the cache pass, from estimates in block times (128 rows by
+// 128 keys, 0.9 us).  `join` is what a part's rows cost the join, written and read (about
+// 7.2 MB a block time).  The caches, taken as half full (the lengths are on the device), cost
+// their bytes at 5.9 MB a block time, or a worker its share of the tiles, 0.5 (8 rows) to 1.9
+// (64 rows) each and 0.6 of that with d = 64, and of the planes' starts and ends, 2.5 (4 rows)
+// to 5.5 (16 rows) each, as fitted to 52 to 148 workers alone.
+//   In turn: 148 workers, then the parts.  With c = items * parts CTAs the parts take about
+//   blocks / parts when c <= 148, or items * blocks / 148 and half a part of tail when there
+//   are more, and in either case 3 for a part's start and end; 13 for the launches and the
+//   join, up to 8 more when the caches keep the SMs from the parts.
+//   Beside one another: a part's CTA and a worker have an SM each, parts and workers 148 together
+//   and at least 52 workers.
+// 8,192 prefix keys and 32 caches of up to 1,024 (8 heads of 128, 32 query heads): 35.8 us in
+// turn, 29 to 31 beside with 4 to 6 parts; 30,000 keys, 40 query heads: 55.9 and 53; 65,531 keys
+// and 96 caches of up to 4,096: 311 and 290; 462 keys, 83 tiny caches of 12 heads: 42 and 66.
+static void prefix_split(const lva_shared_prefix_params* p, int* parts, int* workers) {
+  *workers = kCacheWorkers;
+  *parts = 0;
+  if (p->prefix_len == 0) return;
+  const int group = p->q_heads / p->kv_heads, tok = 128 / group, rows = group * p->steps;
   const double items = double((int64_t(p->B) * p->steps + tok - 1) / tok * p->kv_heads);
   const int64_t blocks = (p->prefix_len + 127) / 128;
   const double join = double(p->B) * p->steps * p->q_heads * (p->d * 8 + 8) / 7.2e6;
-  int best = 1;
-  double best_cost = 0;
+  const double planes = p->capacity > 0 ? double(p->B) * p->kv_heads : 0;
+  const double bytes = planes * p->capacity * p->d * 2 / 5.9e6;
+  const int padded = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const double tile = (0.35 + 0.024 * padded) * (p->d == 64 ? 0.6 : 1.0);
+  const double work = planes * (double(p->capacity / 128 + 1) * tile + 1.5 + 0.25 * rows);
+  auto caches = [&](double n) { return bytes > work / n ? bytes : work / n; };
+  const double all = caches(kCacheWorkers), kept = 2 * all < 8 ? 2 * all : 8;
+  double best = 0;
   for (int s = 1; s <= 32 && s <= blocks; ++s) {
     const double part = double((blocks + s - 1) / s), load = items * s / 148;
-    const double cost = (load <= 1 ? part : items * blocks / 148 + part / 2) + 3 * (load > 1 ? load : 1) + join * s;
-    if (s == 1 || cost < best_cost) { best = s; best_cost = cost; }
+    const double turn = all + (load <= 1 ? part : items * blocks / 148 + part / 2) + 3 * (load > 1 ? load : 1) + join * s + 13 + kept;
+    if (s == 1 || turn < best) { best = turn; *parts = s; *workers = kCacheWorkers; }
+    const double left = kCacheWorkers - items * s;
+    if (p->capacity == 0 || left < 52) continue;
+    const double own = caches(left), beside = (part > own ? part : own) + join * s + 18;
+    if (beside < best) { best = beside; *parts = s; *workers = int(left); }
   }
-  return best;
 }
 
 // Byte offsets of the workspace's pieces (256-byte steps).
 struct PrefixWorkspace {
-  int parts;
+  int parts, workers;
   int64_t part_o, part_lse, own_o, own_lse, scores, score_stride, bytes;
 };
 
@@ -566,7 +588,7 @@ static lva_status prefix_plan(const lva_shared_prefix_params* p, bool with_weigh
       planes * rows / 4 + 1 + planes * chunks >= most || planes * (p->capacity / 64 + 6) >= most)
     return fail(LVA_ERR_UNSUPPORTED, "shared_prefix: B * kv_heads * capacity and B * steps * q_heads must be < 2^31");
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  w->parts = prefix_parts(p);
+  prefix_split(p, &w->parts, &w->workers);
   const int64_t part_rows = int64_t(w->parts) * planes * rows;
   const int64_t own_rows = p->capacity > 0 ? (planes + kCacheWorkers) * rows : 0;
   w->score_stride = (p->capacity + 63) / 64 * 64;
@@ -619,7 +641,7 @@ lva_status lva_shared_prefix_attn(const lva_shared_prefix_params* p, const void*
                   p->o_token_stride, p->o_head_stride, p->scale, w.parts, part_o, part_lse,
                   reinterpret_cast<float*>(ws + w.own_o), reinterpret_cast<float*>(ws + w.own_lse),
                   weight != nullptr ? reinterpret_cast<float*>(ws + w.scores) : nullptr, w.score_stride,
-                  kCacheWorkers, err};
+                  w.workers, err};
   if (p->capacity > 0) {
     const cudaError_t e = launch_cache_attn(c, stream, &why);
     if (e != cudaSuccess) return fail(LVA_ERR_CUDA, "shared_prefix: %s: %s", why, cudaGetErrorString(e));

@@ -18,10 +18,9 @@
 //
 // With a prefix there are two kinds of work: the prefix parts (packed.cu) are bound by the
 // SMs' softmax rate, the caches by HBM.  The caches' kernel goes first, the prefix parts are a
-// programmatic dependent launch (neither reads what the other writes) and take over its SMs one
-// by one as its workers end; the join waits for both.  With the caches on 74 SMs and the parts
-// on the others from the start, the caches took 205 us instead of 146 (64 sequences of up to
-// 8,000 keys, 8 heads of 128) and the parts gained less than that.
+// programmatic dependent launch (neither reads what the other writes), the join waits for
+// both.  The parts run on SMs that the caches' workers were not given, or take over the
+// workers' one by one as they end; the entry point estimates which is shorter.
 //
 //   cache_attn_kernel  the last warp: TMA producer (K and V tiles of 64 keys in one ring, the
 //                      plane's Q rows in two slots); the others: mma.sync m16n8k16 on swizzled
