@@ -7,7 +7,7 @@
 // Eviction, per (sequence, key/value head) of n > budget live entries: the first `sinks` and
 // the last `recent` entries stay, and of the others the budget - sinks - recent of largest
 // weight (ties to the lower index), in their order.
-//   rank_kernel    one CTA per plane of up to 1,024 entries: ranks by comparing all pairs.
+//   rank_kernel    one CTA per plane of up to 640 entries: ranks by comparing all pairs.
 //   select_kernel  one CTA per longer plane: the k-th largest weight by three radix passes over an
 //                  order-preserving 32-bit key (11 + 11 + 10 bits; the first digit is sign,
 //                  exponent and two mantissa bits, so a bin holds a quarter octave and few
@@ -39,7 +39,8 @@ struct AppendParams {
   float* weight;
   const int32_t* lens;
   int32_t* lens_out;
-  int steps, kv_heads, units;        // units: 16-byte units per row
+  int steps, kv_heads, units;        // units: 16-byte units per row, 8 or 16
+  uint32_t hop_heads, hop_tokens;    // kAppendThreads / units rows as heads and tokens
   int64_t capacity;
   int64_t k_token, k_head, v_token, v_head;   // bytes
   int write_lens;
@@ -48,7 +49,7 @@ struct AppendParams {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendPer = 8;        // 16-byte units per thread
+constexpr int kAppendPer = 4;        // 16-byte units per thread
 
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
   const int b = int(blockIdx.x / p.blocks);
@@ -56,27 +57,30 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   const int32_t n = p.lens[b];       // read before lens_out, which may be lens, is written below
   const bool fits = n >= 0 && int64_t(n) + p.steps <= p.capacity;
   if (!fits && part == 0 && threadIdx.x == 0) report_fault(p.err, 3, b);
-  if (fits) {
-    // units of K, then of V: (head, token, unit), the unit fastest; below 2^31 of them
-    const uint32_t half = uint32_t(p.kv_heads) * p.steps * p.units;
+  if (fits && p.steps > 0) {
+    // units of K, then of V: (head, token, unit), the unit fastest; below 2^31 of them.  A
+    // thread's units are kAppendThreads apart: the same unit of rows `hop` apart.
+    const uint32_t rows = 2u * p.kv_heads * p.steps;
     const uint32_t first = part * (kAppendThreads * kAppendPer) + threadIdx.x;
+    const uint32_t unit = first & uint32_t(p.units - 1), hop = uint32_t(kAppendThreads) / uint32_t(p.units);
+    uint32_t row = first / uint32_t(p.units), h = row / uint32_t(p.steps), t = row - h * p.steps;
     uint4 v[kAppendPer];
     uint8_t* dst[kAppendPer];
 #pragma unroll
-    for (int i = 0; i < kAppendPer; ++i) {
-      const uint32_t x = first + i * kAppendThreads;
+    for (int i = 0; i < kAppendPer; ++i, row += hop) {
       dst[i] = nullptr;
-      if (x < 2 * half) {
-        const bool is_v = x >= half;
-        const uint32_t y = is_v ? x - half : x;
-        const uint32_t row = y / uint32_t(p.units), unit = y - row * p.units;
-        const uint32_t h = row / uint32_t(p.steps), t = row - h * p.steps;
-        const uint8_t* src = is_v ? p.v_new + (int64_t(b) * p.steps + t) * p.v_token + h * p.v_head
-                                  : p.k_new + (int64_t(b) * p.steps + t) * p.k_token + h * p.k_head;
+      if (row < rows) {
+        const bool is_v = h >= uint32_t(p.kv_heads);
+        const uint32_t head = is_v ? h - p.kv_heads : h;
+        const uint8_t* src = is_v ? p.v_new + (int64_t(b) * p.steps + t) * p.v_token + head * p.v_head
+                                  : p.k_new + (int64_t(b) * p.steps + t) * p.k_token + head * p.k_head;
         v[i] = __ldg(reinterpret_cast<const uint4*>(src) + unit);
         dst[i] = (is_v ? p.v_cache : p.k_cache) +
-                 (((int64_t(b) * p.kv_heads + h) * p.capacity + n + t) * p.units + unit) * 16;
+                 (((int64_t(b) * p.kv_heads + head) * p.capacity + n + t) * p.units + unit) * 16;
       }
+      h += p.hop_heads;
+      t += p.hop_tokens;
+      if (t >= uint32_t(p.steps)) { t -= p.steps; ++h; }
     }
 #pragma unroll
     for (int i = 0; i < kAppendPer; ++i)
@@ -145,12 +149,16 @@ constexpr int kPer = 4;                              // rounds of 32 entries per
 constexpr int kTileEntries = kSelThreads * kPer;
 constexpr int kKeepTiles = 4;                        // tiles a CTA holds in registers
 
-// Up to 1,024 candidates, one a thread: an entry's rank is the number of entries before it
-// (larger, or equal with a lower index), counted by a walk over all keys in shared memory.  160
-// entries: 4 us against 8.6 us for the radix passes.
-__global__ void __launch_bounds__(kSelThreads) evict_rank_kernel(const SelectParams p) {
-  __shared__ __align__(16) uint32_t keys[kSelThreads];
-  __shared__ uint32_t count[kSelWarps];
+// Short caches, an entry a thread: an entry's rank is the number of entries before it (larger, or
+// equal with a lower index), counted by a walk over all keys in shared memory.  The walk grows
+// with the square of the entries; with the move, against the radix passes: 160 entries 5.5 and
+// 12.9 us (8 planes), 512 entries 9.1 and 13.0, 768 entries 14.3 and 13.1; 512 planes of 512
+// entries 33 and 53, of 768 entries 66 and 63.
+constexpr int kRankMost = 640;
+
+__global__ void __launch_bounds__(kRankMost) evict_rank_kernel(const SelectParams p) {
+  __shared__ __align__(16) uint32_t keys[kRankMost];
+  __shared__ uint32_t count[kRankMost / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t plane = blockIdx.x;
   const int b = int(plane / p.kv_heads);
@@ -171,11 +179,26 @@ __global__ void __launch_bounds__(kSelThreads) evict_rank_kernel(const SelectPar
   for (int j = tid; j < sinks; j += threads) kept[j] = j;
   for (int j = tid; j < recent; j += threads) kept[p.budget - recent + j] = n - recent + j;
   __syncthreads();
+  // Entries of lower warps come first when equal, of higher warps when larger; a warp's own by
+  // both.  keys[] past the last candidate is 0: never larger, and no lower warp's.
   uint32_t rank = 0;
+  const uint4* four = reinterpret_cast<const uint4*>(keys);
+  const int quads = (middle + 3) / 4;
+  if (warp * 32 < middle) {
 #pragma unroll 4
-  for (int j = 0; j < middle; ++j) {
-    const uint32_t other = keys[j];
-    rank += (other > mine || (other == mine && j < tid)) ? 1u : 0u;
+    for (int j = 0; j < warp * 8; ++j) {
+      const uint4 x = four[j];
+      rank += (x.x >= mine) + (x.y >= mine) + (x.z >= mine) + (x.w >= mine);
+    }
+    for (int j = 0; j < 32; ++j) {
+      const uint32_t other = keys[warp * 32 + j];
+      rank += other > mine || (other == mine && j < lane);
+    }
+#pragma unroll 4
+    for (int j = warp * 8 + 8; j < quads; ++j) {
+      const uint4 x = four[j];
+      rank += (x.x > mine) + (x.y > mine) + (x.z > mine) + (x.w > mine);
+    }
   }
   const bool stays = tid < middle && rank < k;
   const unsigned mask = __ballot_sync(0xffffffffu, stays);
@@ -466,6 +489,9 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   p.steps = a.steps;
   p.kv_heads = a.kv_heads;
   p.units = a.d / 8;
+  const int hop = kAppendThreads / p.units;
+  p.hop_heads = a.steps > 0 ? uint32_t(hop / a.steps) : 0;
+  p.hop_tokens = a.steps > 0 ? uint32_t(hop % a.steps) : 0;
   p.capacity = a.capacity;
   p.k_token = a.k_token * 2;
   p.k_head = a.k_head * 2;
@@ -489,7 +515,7 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const int64_t planes = int64_t(a.B) * a.kv_heads;
   const SelectParams s{a.weight, a.lens, a.kept, a.kv_heads, a.capacity, a.budget, a.sinks, a.recent, a.err};
-  if (a.capacity <= kSelThreads)
+  if (a.capacity <= kRankMost)
     evict_rank_kernel<<<unsigned(planes), unsigned((a.capacity + 31) / 32 * 32), 0, stream>>>(s);
   else if (a.capacity <= kKeepTiles * kTileEntries) evict_select_kernel<true><<<unsigned(planes), kSelThreads, 0, stream>>>(s);
   else evict_select_kernel<false><<<unsigned(planes), kSelThreads, 0, stream>>>(s);

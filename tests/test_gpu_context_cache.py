@@ -268,6 +268,9 @@ def weights_like(g, kind, *shape):
     (2, 2, 64, 40, [0, 40], 40, 2, 2),
     (2, 2, 128, 9000, [9000, 5001], 5000, 4, 500),
     (4, 5, 128, 700, [700, 699, 300, 650], 301, 1, 0),
+    (1, 2, 64, 640, [640], 400, 3, 100),
+    (2, 1, 64, 641, [641, 500], 400, 0, 0),
+    (2, 2, 128, 609, [609, 608], 300, 1, 33),
     (1, 2, 64, 1024, [1024], 700, 3, 100),
     (2, 1, 64, 1025, [1025, 701], 700, 0, 0),
     (2, 1, 64, 16384, [16384, 4097], 4096, 1, 1),
