@@ -13,14 +13,14 @@
 //                  exponent and two mantissa bits, so a bin holds a quarter octave and few
 //                  lanes of a warp meet in one), then one ordered pass with ballots that
 //                  writes the kept indices.
-//   move_kernel    out of place: a CTA per 64 kept rows, all independent.
+//   move_kernel    out of place: a CTA per 64 kept rows, all independent; launched while the
+//                  ranking runs, waits for its end (two launches in a row cost 1 to 2 us more).
 //   move_in_place_kernel   rows only ever move down (the j-th kept index is >= j).  A CTA owns
 //                  a column slice of one plane's K or V and walks the kept rows in ascending
 //                  chunks, loads of the next chunks in flight: chunk i's sources are all
 //                  loaded before it stores to rows [i C, (i + 1) C), and a later chunk's
 //                  sources lie at or above its own rows, so no row is overwritten unread.
-//                  Column slices keep CTAs independent; there are enough of them to fill the
-//                  GPU from 19 planes on.
+//                  Column slices keep CTAs independent.
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -157,6 +157,7 @@ constexpr int kKeepTiles = 4;                        // tiles a CTA holds in reg
 constexpr int kRankMost = 640;
 
 __global__ void __launch_bounds__(kRankMost) evict_rank_kernel(const SelectParams p) {
+  launch_dependents();                               // the move's CTAs get ready
   __shared__ __align__(16) uint32_t keys[kRankMost];
   __shared__ uint32_t count[kRankMost / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -213,6 +214,7 @@ __global__ void __launch_bounds__(kRankMost) evict_rank_kernel(const SelectParam
 // all loads in flight, and serve every pass; otherwise each pass reads them again (from L2).
 template <bool KEEP>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
+  launch_dependents();                               // the move's CTAs get ready
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t warp_sum[kSelWarps];
   __shared__ uint2 counts[kKeepTiles * kSelWarps];   // entries above and at the threshold, per tile and warp
@@ -368,6 +370,7 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 64;
 
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
+  wait_prerequisites();                              // kept is written, lens has been read
   const int64_t blocks = (p.budget + kMoveRows - 1) / kMoveRows;
   const int64_t plane = blockIdx.x / blocks;
   const int64_t j0 = (blockIdx.x - plane * blocks) * kMoveRows;
@@ -537,13 +540,15 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   p.capacity = a.capacity;
   p.budget = a.budget;
   if (a.k_out == a.k_cache) {
-    // Slices of at least 32 bytes (a DRAM sector), as many as fill the GPU about twice.
+    // Slices of at least 32 bytes (a DRAM sector) until there are three CTAs for an SM: 96
+    // planes of 8,192 kept rows 184 us with slices of 128 bytes, 154 with 64; 64 planes of
+    // 20,000 rows 272 with 64 bytes, 290 with 32; 32 planes of 8,192 rows 74 and 69.
     p.slices = 1;
-    while (p.slices < p.units / 2 && planes * 2 * p.slices < 2 * sm_count()) p.slices *= 2;
+    while (p.slices < p.units / 2 && planes * 2 * p.slices < 3 * sm_count()) p.slices *= 2;
     move_in_place_kernel<<<unsigned(planes * (2 * p.slices + 1)), kMoveThreads, 0, stream>>>(p);
   } else {
     p.slices = 0;
-    move_kernel<<<unsigned(planes * ((a.budget + kMoveRows - 1) / kMoveRows)), kMoveThreads, 0, stream>>>(p);
+    return launch_dependent(move_kernel, unsigned(planes * ((a.budget + kMoveRows - 1) / kMoveRows)), kMoveThreads, 0, stream, p);
   }
   return cudaGetLastError();
 }
