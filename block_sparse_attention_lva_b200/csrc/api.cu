@@ -670,6 +670,12 @@ static lva_status check_cache(const char* fn, int B, int kv_heads, int64_t capac
   return LVA_OK;
 }
 
+// Whether [a, a + n) and [b, b + n) share a byte.
+static bool overlap(const void* a, const void* b, int64_t n) {
+  const intptr_t x = reinterpret_cast<intptr_t>(a), y = reinterpret_cast<intptr_t>(b);
+  return x < y + n && y < x + n;
+}
+
 lva_status lva_append_cache(const void* k_new, const void* v_new, int64_t k_token_stride, int64_t k_head_stride,
                             int64_t v_token_stride, int64_t v_head_stride, void* k_cache, void* v_cache,
                             float* weight, const int32_t* lens, int32_t* lens_out, int B, int steps, int kv_heads,
@@ -681,7 +687,7 @@ lva_status lva_append_cache(const void* k_new, const void* v_new, int64_t k_toke
     return fail(LVA_ERR_INVALID_ARG, "append: strides must be multiples of 8 elements, at least d");
   const int64_t most = int64_t(1) << 31;
   const int64_t units = int64_t(kv_heads) * steps;               // rows of one sequence, K or V
-  if (units >= most / 32 || units * 32 / 2048 + 1 >= most / (B > 0 ? B : 1))
+  if (units >= most / 32 || units * 32 / kAppendUnits + 1 >= most / (B > 0 ? B : 1))
     return fail(LVA_ERR_UNSUPPORTED, "append: too many rows for one launch");
   if (B == 0) return ok();
   if (!lens || !lens_out || (steps > 0 && (!k_new || !v_new || (capacity > 0 && (!k_cache || !v_cache)))))
@@ -690,17 +696,13 @@ lva_status lva_append_cache(const void* k_new, const void* v_new, int64_t k_toke
     return fail(LVA_ERR_INVALID_ARG, "append: rows and caches must be 16-byte aligned");
   if (!aligned(weight, 4) || !aligned(lens, 4) || !aligned(lens_out, 4))
     return fail(LVA_ERR_INVALID_ARG, "append: weight and lens must be 4-byte aligned");
+  if (lens_out != lens && overlap(lens, lens_out, int64_t(B) * 4))
+    return fail(LVA_ERR_INVALID_ARG, "append: lens_out must be lens or apart from it");
   int* err = device_error_word();
   if (err == nullptr) return fail(LVA_ERR_CUDA, "append: cannot locate the device error word");
   AppendArgs a{k_new, v_new, k_cache, v_cache, weight, lens, lens_out, B, steps, kv_heads, d, capacity,
                k_token_stride, k_head_stride, v_token_stride, v_head_stride, err};
   return from_cuda(launch_append(a, stream), "append launch");
-}
-
-// Whether [a, a + n) and [b, b + n) share a byte.
-static bool overlap(const void* a, const void* b, int64_t n) {
-  const intptr_t x = reinterpret_cast<intptr_t>(a), y = reinterpret_cast<intptr_t>(b);
-  return x < y + n && y < x + n;
 }
 
 lva_status lva_evict_cache(const void* k_cache, const void* v_cache, const float* weight, const int32_t* lens,
@@ -722,6 +724,8 @@ lva_status lva_evict_cache(const void* k_cache, const void* v_cache, const float
     return fail(LVA_ERR_INVALID_ARG, "evict: caches must be 16-byte aligned");
   if (!aligned(weight, 4) || !aligned(weight_out, 4) || !aligned(lens, 4) || !aligned(lens_out, 4) || !aligned(kept, 4))
     return fail(LVA_ERR_INVALID_ARG, "evict: weight, lens and kept must be 4-byte aligned");
+  if (lens_out != lens && overlap(lens, lens_out, int64_t(B) * 4))
+    return fail(LVA_ERR_INVALID_ARG, "evict: lens_out must be lens or apart from it");
   const int64_t bytes = planes * capacity * d * 2;
   const bool in_k = k_out == k_cache, in_v = v_out == v_cache, in_w = weight_out == weight;
   if (in_k != in_v || in_k != in_w)

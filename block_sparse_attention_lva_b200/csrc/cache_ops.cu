@@ -49,7 +49,7 @@ struct AppendParams {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendPer = 4;        // 16-byte units per thread
+constexpr int kAppendPer = kAppendUnits / kAppendThreads;
 
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
   const int b = int(blockIdx.x / p.blocks);
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     // units of K, then of V: (head, token, unit), the unit fastest; below 2^31 of them.  A
     // thread's units are kAppendThreads apart: the same unit of rows `hop` apart.
     const uint32_t rows = 2u * p.kv_heads * p.steps;
-    const uint32_t first = part * (kAppendThreads * kAppendPer) + threadIdx.x;
+    const uint32_t first = part * kAppendUnits + threadIdx.x;
     const uint32_t unit = first & uint32_t(p.units - 1), hop = uint32_t(kAppendThreads) / uint32_t(p.units);
     uint32_t row = first / uint32_t(p.units), h = row / uint32_t(p.steps), t = row - h * p.steps;
     uint4 v[kAppendPer];
@@ -502,7 +502,7 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   p.v_head = a.v_head * 2;
   p.err = a.err;
   const int64_t units = 2 * int64_t(a.kv_heads) * a.steps * p.units;
-  int64_t blocks = (units + kAppendThreads * kAppendPer - 1) / (kAppendThreads * kAppendPer);
+  int64_t blocks = (units + kAppendUnits - 1) / kAppendUnits;
   if (blocks < 1) blocks = 1;        // no token: lens_out alone
   // In place with several CTAs per sequence, the lengths advance in a launch of their own.
   const bool later = a.lens_out == a.lens && blocks > 1;

@@ -251,6 +251,7 @@ constexpr int kCacheWorkers = 148;
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream, const char** why);
 cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream);
 
+constexpr int kAppendUnits = 1024;   // 16-byte units a CTA of the append copies
 struct AppendArgs {
   const void* k_new;
   const void* v_new;

@@ -590,9 +590,9 @@ lva_status lva_shared_prefix_attn(const lva_shared_prefix_params* params, const 
  *
  * Row lens[b] + t of every head of sequence b's caches takes token t of k_new, v_new, its
  * weight (weight: NULL or fp32 [B, kv_heads, capacity]) becomes 0, and lens_out[b] =
- * lens[b] + steps.  lens_out may be lens.  A sequence whose cache is too full (or whose
- * length is negative) is left as it is, lens_out[b] = lens[b], and reported through
- * lva_device_error as LVA_ERR_CAPACITY (detail = the sequence).
+ * lens[b] + steps.  lens_out is lens or shares no byte with it.  A sequence whose cache is too
+ * full (or whose length is negative) is left as it is, lens_out[b] = lens[b], and reported
+ * through lva_device_error as LVA_ERR_CAPACITY (detail = the sequence).
  *
  * k_new, v_new: device, bf16, element (token b*steps + t, head h, e) at
  * (b*steps + t) * token_stride + h * head_stride + e, strides in elements, multiples of 8;
@@ -619,8 +619,8 @@ lva_status lva_append_cache(const void* k_new, const void* v_new, int64_t k_toke
  * The kept rows, weights and lengths go to k_out, v_out, weight_out (shaped like k_cache,
  * v_cache, weight) and lens_out; rows past a sequence's new length are left as they were.
  * In place (k_out == k_cache, v_out == v_cache, weight_out == weight, all three or none) rows
- * move down within the caches; otherwise outputs and inputs must not overlap.  lens_out may be
- * lens either way.  kept: device, int32 [B, kv_heads, budget]: the old index of every kept
+ * move down within the caches; otherwise outputs and inputs must not overlap.  lens_out is
+ * lens, either way, or shares no byte with it.  kept: device, int32 [B, kv_heads, budget]: the old index of every kept
  * row (identity and then -1 for a sequence below its budget).
  *
  * A length outside [0, capacity] is reported through lva_device_error as LVA_ERR_INVALID_ARG

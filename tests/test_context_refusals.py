@@ -145,7 +145,8 @@ def append(kn=16, vn=16, kc=16, vc=16, weight=None, lens=4, lens_out=4, ks=128, 
     (dict(cap=1 << 31), UNSUPPORTED), (dict(steps=1 << 30), UNSUPPORTED), (dict(B=1 << 30, steps=1 << 10), UNSUPPORTED),
     (dict(ks=60), INVALID), (dict(kh=12), INVALID), (dict(vs=132), INVALID), (dict(vh=0), INVALID),
     (dict(kn=8), INVALID), (dict(vn=4), INVALID), (dict(kc=8), INVALID), (dict(vc=24), INVALID), (dict(weight=3), INVALID),
-    (dict(lens=2), INVALID), (dict(lens_out=2), INVALID),
+    (dict(lens=2), INVALID), (dict(lens_out=2), INVALID), (dict(lens_out=8), INVALID), (dict(lens=8), INVALID),
+    (dict(B=1 << 16, steps=1 << 20, hk=1), UNSUPPORTED),       # 2^31 CTAs
     (dict(kn=None), INVALID), (dict(vc=None), INVALID), (dict(lens=None), INVALID), (dict(lens_out=None), INVALID),
     (dict(B=0, kn=None), OK),
 ])
@@ -170,7 +171,7 @@ def evict(k=MB, v=2 * MB, w=3 * MB, lens=4, ko=4 * MB, vo=5 * MB, wo=6 * MB, lo=
     (dict(sinks=21), INVALID), (dict(sinks=10, recent=11), INVALID), (dict(recent=1 << 62), INVALID),
     (dict(B=1 << 28), UNSUPPORTED), (dict(cap=1 << 31), UNSUPPORTED),
     (dict(k=None), INVALID), (dict(w=None), INVALID), (dict(lens=None), INVALID), (dict(vo=None), INVALID), (dict(lo=None), INVALID),
-    (dict(kept=None), INVALID),
+    (dict(kept=None), INVALID), (dict(lo=8), INVALID),
     (dict(k=MB + 8), INVALID), (dict(vo=5 * MB + 2), INVALID), (dict(w=3 * MB + 2), INVALID), (dict(kept=2), INVALID),
     # in place: all three or none
     (dict(ko=MB), INVALID), (dict(ko=MB, vo=2 * MB), INVALID), (dict(wo=3 * MB), INVALID),
