@@ -101,6 +101,7 @@ SHAPES = {
     "rows_64": (2, 64, 2, 2, 64, 70, 190, [190, 63]),
     "long_prefix": (5, 1, 10, 2, 128, 5000, 70, [1, 2, 3, 70, 9]),
     "long_cache": (2, 1, 4, 1, 128, 3, 30000, [29999, 17]),
+    "many_planes": (83, 1, 60, 12, 64, 462, 24, [(5 * i) % 25 for i in range(83)]),
     "many_sequences": (150, 1, 2, 1, 64, 20, 80, [(7 * i) % 81 for i in range(150)]),
 }
 
@@ -199,7 +200,8 @@ def test_cache_past_32_bit_offsets():
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("B,T,hk,d,cap,lens", [
     (3, 1, 2, 64, 9, [0, 8, 4]), (2, 5, 3, 128, 40, [0, 35]), (2, 200, 4, 128, 500, [7, 300]), (1, 0, 1, 64, 4, [3]),
-    (70, 1, 8, 128, 5, [i % 5 for i in range(70)]),
+    (70, 1, 8, 128, 5, [i % 5 for i in range(70)]), (2, 7, 12, 64, 60, [50, 3]), (2, 33, 5, 64, 90, [1, 57]),
+    (3, 17, 8, 128, 40, [23, 0, 5]), (1, 31, 3, 64, 100, [9]), (2, 1560, 3, 128, 1700, [100, 0]),
 ])
 def test_append(B, T, hk, d, cap, lens, in_place):
     import block_sparse_attention_lva_b200 as lva
