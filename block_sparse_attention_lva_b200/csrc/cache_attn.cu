@@ -658,23 +658,27 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-// log2 sum_j 2^(LSE_j) over a row's parts (whole warp); -inf when none has a key.
-__device__ __forceinline__ float join_lse(const JoinParams& p, const Parts& x) {
+// log2 sum_j 2^(LSE_j) over a row's parts (whole warp; mine: part lane's); -inf when none has a key.
+__device__ __forceinline__ float join_lse(const JoinParams& p, const Parts& x, float mine) {
   const int lane = threadIdx.x & 31;
-  float top = -INFINITY;
-  for (int j = lane; j < x.count; j += 32) top = fmaxf(top, x.lse(p, j));
+  float top = mine;
+  for (int j = lane + 32; j < x.count; j += 32) top = fmaxf(top, x.lse(p, j));
   top = warp_max(top);
   const float use = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
-  for (int j = lane; j < x.count; j += 32) sum += ex2_approx(x.lse(p, j) - use);
+  float sum = ex2_approx(mine - use);
+  for (int j = lane + 32; j < x.count; j += 32) sum += ex2_approx(x.lse(p, j) - use);
   sum = warp_sum(sum);
   return sum == 0.f ? -INFINITY : use + __log2f(sum);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) {
+// WEIGHTS: blocks for the weights follow those of the rows.  SMALL: fewer O parts in flight, so that
+// eight blocks fit an SM instead of four, for long lists of blocks over few parts (16 caches of
+// up to 6,000 keys, 12 heads, 4 tokens: the call takes 77 us, 80 in the other form; 2 tokens over
+// 5,448 shared keys in 22 parts take 23 us so, 21 in the other).
+template <int D, bool WEIGHTS, bool SMALL>
+__global__ void __launch_bounds__(kJoinThreads, SMALL ? 8 : 4) join_kernel(const JoinParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (int(blockIdx.x) < p.row_blocks) {
+  if (!WEIGHTS || int(blockIdx.x) < p.row_blocks) {
     // One warp per row: O and LSE.
     const uint32_t row = blockIdx.x * (kJoinThreads / 32) + warp;
     if (row >= uint32_t(p.B) * p.kv_heads * p.rows) return;
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
     const Parts x = parts_of(p, b, kvh, r, n, Runs(total, p.workers), before);
     const int t = r / p.group, head = kvh * p.group + (r - t * p.group);
     wait_prerequisites();                          // the caller's lengths needed no wait
-    constexpr int V = D / 32, AHEAD = 16;
+    constexpr int V = D / 32, AHEAD = SMALL ? 4 : 16;
     auto load = [&](int j, float (&v)[V]) {
       const float* src = (j < x.splits ? p.part_o : p.own_o) + x.at(p, j) * D + lane * V;
       if constexpr (V == 4) {
@@ -712,7 +716,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
       const float sum = warp_sum(ex2_approx(mine - use));
       lse = sum == 0.f ? -INFINITY : use + __log2f(sum);
     } else {
-      lse = join_lse(p, x);
+      lse = join_lse(p, x, mine);
     }
     const float use = lse == -INFINITY ? 0.f : lse;
     float acc[V] = {};
@@ -757,29 +761,58 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const JoinParams p) 
   const int total = count_cost(p.lens, p.B, p.capacity, b, &before) * p.kv_heads;
   const Runs runs(total, p.workers);
   wait_prerequisites();
-  for (int r = warp; r < p.rows; r += kJoinThreads / 32) {
-    const float lse = join_lse(p, parts_of(p, b, kvh, r, n, runs, before));
-    if (lane == 0) row_lse[r] = lse == -INFINITY ? 0.f : lse;      // no weight: every score is -inf
-  }
+  // The weights so far and the first rows' scores are on their way while the rows' LSE is joined.
+  constexpr int AHEAD = 4;
   const int key = chunk * kChunk + threadIdx.x * 4;
-  const int base = n - p.steps + 1;
-  float sum[4] = {}, old[4] = {};
+  float old[4] = {};
   float* w = p.weight + plane * p.capacity + key;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (key + e < n) old[e] = w[e];
+  const float* src = p.scores + int64_t(plane) * p.rows * p.score_stride + key;
+  float4 next[AHEAD];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (r0 + i < p.rows && key < n) next[i] = *reinterpret_cast<const float4*>(src + (r0 + i) * p.score_stride);
+  };
+  load(0);
+  // Four rows a warp, eight lanes over each row's parts (all rows of a plane have as many).
+  for (int r0 = warp * 4; r0 < p.rows; r0 += kJoinThreads / 8) {
+    const int r = r0 + lane / 8, l8 = lane % 8;
+    const Parts x = parts_of(p, b, kvh, r < p.rows ? r : 0, n, runs, before);
+    const float mine = l8 < x.count ? x.lse(p, l8) : -INFINITY;
+    float top = mine;
+    for (int j = l8 + 8; j < x.count; j += 8) top = fmaxf(top, x.lse(p, j));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    const float use = top == -INFINITY ? 0.f : top;
+    float sum = ex2_approx(mine - use);
+    for (int j = l8 + 8; j < x.count; j += 8) sum += ex2_approx(x.lse(p, j) - use);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    // no weight where no part has a key: every score is -inf
+    if (l8 == 0 && r < p.rows) row_lse[r] = sum == 0.f ? 0.f : use + __log2f(sum);
+  }
   __syncthreads();
   if (key >= n) return;
-  const float* src = p.scores + int64_t(plane) * p.rows * p.score_stride + key;
-#pragma unroll 4
-  for (int r = 0; r < p.rows; ++r) {
-    const float4 f = *reinterpret_cast<const float4*>(src + r * p.score_stride);
-    const int lim = base + r / p.group;            // keys this row sees
-    const float lse = row_lse[r];
-    if (key < lim) sum[0] += ex2_approx(f.x - lse);
-    if (key + 1 < lim) sum[1] += ex2_approx(f.y - lse);
-    if (key + 2 < lim) sum[2] += ex2_approx(f.z - lse);
-    if (key + 3 < lim) sum[3] += ex2_approx(f.w - lse);
+  const int base = n - p.steps + 1;
+  float sum[4] = {};
+  for (int r0 = 0; r0 < p.rows; r0 += AHEAD) {
+    float4 f[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) f[i] = next[i];
+    load(r0 + AHEAD);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (r0 + i < p.rows) {
+        const int lim = base + (r0 + i) / p.group;   // keys this row sees
+        const float lse = row_lse[r0 + i];
+        if (key < lim) sum[0] += ex2_approx(f[i].x - lse);
+        if (key + 1 < lim) sum[1] += ex2_approx(f[i].y - lse);
+        if (key + 2 < lim) sum[2] += ex2_approx(f[i].z - lse);
+        if (key + 3 < lim) sum[3] += ex2_approx(f[i].w - lse);
+      }
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e)
@@ -835,8 +868,12 @@ cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream) {
   p.row_blocks = int((planes * rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
   p.chunks = a.weight != nullptr ? int((a.capacity + kChunk - 1) / kChunk) : 0;
   const unsigned blocks = unsigned(p.row_blocks + planes * p.chunks);
-  return a.d == 128 ? launch_dependent(join_kernel<128>, blocks, kJoinThreads, 0, stream, p)
-                    : launch_dependent(join_kernel<64>, blocks, kJoinThreads, 0, stream, p);
+  // more blocks than the large form has room for at once, and parts within the small one's loads
+  const bool small = p.chunks > 0 && blocks > 4u * unsigned(sm_count()) && a.splits <= 4;
+  auto launch = [&](auto kernel) { return launch_dependent(kernel, blocks, kJoinThreads, 0, stream, p); };
+  if (small) return a.d == 128 ? launch(join_kernel<128, true, true>) : launch(join_kernel<64, true, true>);
+  if (p.chunks > 0) return a.d == 128 ? launch(join_kernel<128, true, false>) : launch(join_kernel<64, true, false>);
+  return a.d == 128 ? launch(join_kernel<128, false, false>) : launch(join_kernel<64, false, false>);
 }
 
 }  // namespace lva
