@@ -128,8 +128,7 @@ __device__ __forceinline__ void find_bin(const uint32_t* hist, uint32_t k, uint3
   }
   if (lane == 31) warp_sum[warp] = sum;
   __syncthreads();
-  uint32_t base = 0;
-  for (int w = 0; w < warp; ++w) base += warp_sum[w];
+  const uint32_t base = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u);
   const uint32_t before = base + sum - a - b;        // entries in the bins above this thread's
   if (before < k && k <= before + a) { out[0] = kBins - 1 - 2 * tid; out[1] = before; }
   else if (before + a < k && k <= before + a + b) { out[0] = kBins - 2 - 2 * tid; out[1] = before + a; }
@@ -205,8 +204,7 @@ __global__ void __launch_bounds__(kRankMost) evict_rank_kernel(const SelectParam
   const unsigned mask = __ballot_sync(0xffffffffu, stays);
   if (lane == 0) count[warp] = __popc(mask);
   __syncthreads();
-  uint32_t before = 0;
-  for (int v = 0; v < warp; ++v) before += count[v];
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? count[lane] : 0u);
   if (stays) kept[sinks + before + __popc(mask & ((1u << lane) - 1u))] = sinks + tid;
 }
 
