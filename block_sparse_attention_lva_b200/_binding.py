@@ -8,6 +8,7 @@ library's CUDA kernels; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import struct
 from dataclasses import dataclass
@@ -536,6 +537,9 @@ def lva_packed_workspace_bytes(sequences: int, q_heads: int, kv_heads: int, d: i
     return lib.lva_packed_workspace_bytes(_PACKED.pack(sequences, q_heads, kv_heads, d, 1, 1.0, total_q, total_k, *[0] * 8))
 
 
+_packed_size = functools.lru_cache(maxsize=1024)(lva_packed_workspace_bytes)    # by sizes alone
+
+
 def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = True, workspace=None):
     """O, LSE of attention over packed sequences: q, o [total_q, Hq, d], k, v [total_k, Hkv, d]
     (bf16, rows contiguous, token and head strides free), lse [Hq, total_q] (fp32), cu_q and
@@ -559,7 +563,7 @@ def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = Tr
     if workspace is not None:
         ws, size = _bytes_of(workspace, "workspace", cur)
     else:
-        size = lib.lva_packed_workspace_bytes(p)
+        size = _packed_size(n - 1, hq, hk, d, tq, tk)
         if size > 0:
             workspace = torch.empty(size, dtype=_U8, device=q.device)
             ws = workspace.data_ptr()
