@@ -531,14 +531,26 @@ lva_status lva_packed_attn(const lva_packed_params* p, const void* q, const void
 //   blocks / parts when c <= 148, or items * blocks / 148 and half a part of tail when there
 //   are more, and in either case 3 for a part's start and end; 13 for the launches and the
 //   join, up to 8 more when the caches keep the SMs from the parts.
+//   In one list: where all tokens of the batch are at most 32 rows, the prefix can be one more
+//   sequence of the cache pass, at the tiles' cost for that many rows; 12 for two launches
+//   instead of three, 0.12 for each piece that the join finds of a row.  The other forms are
+//   kept unless this one is clearly shorter (the lengths may be above the estimate).
 //   Beside one another: a part's CTA and a worker have an SM each, parts and workers 148 together
 //   and at least 52 workers.
 // 8,192 prefix keys and 32 caches of up to 1,024 (8 heads of 128, 32 query heads): 35.8 us in
 // turn, 29 to 31 beside with 4 to 6 parts; 30,000 keys, 40 query heads: 55.9 and 53; 65,531 keys
 // and 96 caches of up to 4,096: 311 and 290; 462 keys, 83 tiny caches of 12 heads: 42 and 66.
-static void prefix_split(const lva_shared_prefix_params* p, int* parts, int* workers) {
+// 1,050 prefix keys, one cache, 4 rows: 16.3 us beside, 14.1 in one list; 9 keys, two caches, 2
+// rows: 16.4 and 14.0; with 44 to 64 rows 16 to 18 and 17 to 31.
+static double tile_cost(int rows, int d) {
+  const int padded = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return (0.35 + 0.024 * padded) * (d == 64 ? 0.6 : 1.0);
+}
+
+static void prefix_split(const lva_shared_prefix_params* p, int* parts, int* workers, int* with_prefix) {
   *workers = kCacheWorkers;
   *parts = 0;
+  *with_prefix = 0;
   if (p->prefix_len == 0) return;
   const int group = p->q_heads / p->kv_heads, tok = 128 / group, rows = group * p->steps;
   const double items = double((int64_t(p->B) * p->steps + tok - 1) / tok * p->kv_heads);
@@ -546,9 +558,7 @@ static void prefix_split(const lva_shared_prefix_params* p, int* parts, int* wor
   const double join = double(p->B) * p->steps * p->q_heads * (p->d * 8 + 8) / 7.2e6;
   const double planes = p->capacity > 0 ? double(p->B) * p->kv_heads : 0;
   const double bytes = planes * p->capacity * p->d * 2 / 5.9e6;
-  const int padded = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  const double tile = (0.35 + 0.024 * padded) * (p->d == 64 ? 0.6 : 1.0);
-  const double work = planes * (double(p->capacity / 128 + 1) * tile + 1.5 + 0.25 * rows);
+  const double work = planes * (double(p->capacity / 128 + 1) * tile_cost(rows, p->d) + 1.5 + 0.25 * rows);
   auto caches = [&](double n) { return bytes > work / n ? bytes : work / n; };
   const double all = caches(kCacheWorkers), kept = 2 * all < 8 ? 2 * all : 8;
   double best = 0;
@@ -561,11 +571,19 @@ static void prefix_split(const lva_shared_prefix_params* p, int* parts, int* wor
     const double own = caches(left), beside = (part > own ? part : own) + join * s + 18;
     if (beside < best) { best = beside; *parts = s; *workers = int(left); }
   }
+  const double all_rows = double(p->B) * rows;
+  const double tiles = double(p->prefix_len / 64 + 1), list = planes * (p->capacity / 64 + 6) + p->kv_heads * (tiles + 5);
+  if (p->capacity == 0 || all_rows > kListMaxRows || list >= double(int64_t(1) << 31)) return;
+  const double wide = tile_cost(int(all_rows), p->d), places = planes * double(p->capacity / 128 + 6) + p->kv_heads * (tiles + 5);
+  const double pieces = places > kCacheWorkers ? (tiles + 5) * kCacheWorkers / places : tiles;
+  const double one = (planes * (double(p->capacity / 128 + 1) * wide + 1.5 + 0.25 * rows) +
+                      p->kv_heads * (tiles * wide + 1.5 + 0.25 * all_rows)) / kCacheWorkers + 0.12 * pieces + 12;
+  if (1.4 * one < best) { *parts = 0; *workers = kCacheWorkers; *with_prefix = 1; }
 }
 
 // Byte offsets of the workspace's pieces (256-byte steps).
 struct PrefixWorkspace {
-  int parts, workers;
+  int parts, workers, with_prefix;
   int64_t part_o, part_lse, own_o, own_lse, scores, score_stride, bytes;
 };
 
@@ -588,8 +606,8 @@ static lva_status prefix_plan(const lva_shared_prefix_params* p, bool with_weigh
       planes * rows / 4 + 1 + planes * chunks >= most || planes * (p->capacity / 64 + 6) >= most)
     return fail(LVA_ERR_UNSUPPORTED, "shared_prefix: B * kv_heads * capacity and B * steps * q_heads must be < 2^31");
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  prefix_split(p, &w->parts, &w->workers);
-  const int64_t part_rows = int64_t(w->parts) * planes * rows;
+  prefix_split(p, &w->parts, &w->workers, &w->with_prefix);
+  const int64_t part_rows = w->with_prefix ? (p->kv_heads + int64_t(kCacheWorkers)) * p->B * rows : int64_t(w->parts) * planes * rows;
   const int64_t own_rows = p->capacity > 0 ? (planes + kCacheWorkers) * rows : 0;
   w->score_stride = (p->capacity + 63) / 64 * 64;
   w->part_o = 0;
@@ -636,9 +654,10 @@ lva_status lva_shared_prefix_attn(const lva_shared_prefix_params* p, const void*
   float* part_o = reinterpret_cast<float*>(ws + w.part_o);
   float* part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   const char* why = "launch";
-  CacheAttnArgs c{q, k_cache, v_cache, lens, o, lse, p->capacity > 0 ? weight : nullptr, p->B, p->steps, p->q_heads,
+  CacheAttnArgs c{q, prefix_k, prefix_v, k_cache, v_cache, lens, o, lse, p->capacity > 0 ? weight : nullptr, p->B, p->steps, p->q_heads,
                   p->kv_heads, p->d, p->prefix_len, p->capacity, p->q_token_stride, p->q_head_stride,
-                  p->o_token_stride, p->o_head_stride, p->scale, w.parts, part_o, part_lse,
+                  p->k_token_stride, p->k_head_stride, p->v_token_stride, p->v_head_stride,
+                  p->o_token_stride, p->o_head_stride, p->scale, w.parts, w.with_prefix, part_o, part_lse,
                   reinterpret_cast<float*>(ws + w.own_o), reinterpret_cast<float*>(ws + w.own_lse),
                   weight != nullptr ? reinterpret_cast<float*>(ws + w.scores) : nullptr, w.score_stride,
                   w.workers, err};

@@ -20,7 +20,9 @@
 // SMs' softmax rate, the caches by HBM.  The caches' kernel goes first, the prefix parts are a
 // programmatic dependent launch (neither reads what the other writes), the join waits for
 // both.  The parts run on SMs that the caches' workers were not given, or take over the
-// workers' one by one as they end; the entry point estimates which is shorter.
+// workers' one by one as they end; the entry point estimates which is shorter.  A small batch's
+// prefix (all its tokens at most 32 rows) can be one more sequence of the list instead, with
+// all tokens' rows against its tiles (PREFIX), which saves a launch.
 //
 //   cache_attn_kernel  the last warp: TMA producer (K and V tiles of 64 keys in one ring, the
 //                      plane's Q rows in two slots); the others: mma.sync m16n8k16 on swizzled
@@ -63,6 +65,10 @@ struct CacheParams {
   float* scores;
   int64_t score_stride;
   int workers;
+  // PREFIX: the shared prefix is the list's last sequence, all tokens of the batch its rows
+  int prefix_len, prefix_rows;
+  float* part_o;                             // [kv_heads + workers, prefix_rows, D]
+  float* part_lse;
   int* err;
 };
 
@@ -112,6 +118,7 @@ struct Runs {
 
 // Walks a worker's run plane by plane (every warp the same walk).  A plane's tiles come first in
 // its part of the list; a run that meets only the rest of it has no tile there.
+template <bool PREFIX>
 struct Walk {
   const CacheParams& p;
   int left;                  // of the run, not yet handed out
@@ -119,15 +126,16 @@ struct Walk {
   __device__ __forceinline__ Walk(const CacheParams& params, int worker) : p(params) {
     const int lane = threadIdx.x & 31;
     int unused;
-    const Runs runs(count_cost(p.lens, p.B, p.capacity, 0, &unused) * p.kv_heads, p.workers);
+    const int shared = PREFIX ? plane_cost(tiles_of(p.prefix_len)) : 0;
+    const Runs runs((count_cost(p.lens, p.B, p.capacity, 0, &unused) + shared) * p.kv_heads, p.workers);
     left = 0;
     b = kvh = n = tiles = t0 = 0;
     if (worker >= runs.n) return;
     int at = runs.start(worker);
     left = runs.start(worker + 1) - at;
     // the sequence that holds place `at`: 32 sequences at a time
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int mine = b0 + lane < p.B ? live_len(p.lens, b0 + lane, p.capacity) : 0;
+    for (int b0 = 0; b0 < p.B + (PREFIX ? 1 : 0); b0 += 32) {
+      const int mine = keys(b0 + lane);
       const int own = plane_cost(tiles_of(mine)) * p.kv_heads;
       int sum = own;
 #pragma unroll
@@ -151,6 +159,10 @@ struct Walk {
     }
     left = 0;                // not reached: the run lies inside the list
   }
+  __device__ __forceinline__ int keys(int x) const {
+    return x < p.B ? live_len(p.lens, x, p.capacity) : PREFIX && x == p.B ? p.prefix_len : 0;
+  }
+  __device__ __forceinline__ bool in_prefix() const { return PREFIX && b == p.B; }
   // Tiles of the current plane in this run; at least one while left > 0.
   __device__ __forceinline__ int count() const { return left < tiles - t0 ? left : tiles - t0; }
   __device__ __forceinline__ void next() {
@@ -161,10 +173,10 @@ struct Walk {
     kvh = 0;
     do {
       ++b;
-      n = b < p.B ? live_len(p.lens, b, p.capacity) : 0;
+      n = keys(b);
     } while (b < p.B && n == 0);
     tiles = tiles_of(n);
-    if (b >= p.B) left = 0;
+    if (n == 0) left = 0;
   }
 };
 
@@ -227,11 +239,14 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-template <int D, int NT, int WR>
-__global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
-                                                                 const __grid_constant__ CUtensorMap tm_k,
-                                                                 const __grid_constant__ CUtensorMap tm_v,
-                                                                 const CacheParams p) {
+struct CacheMaps {
+  CUtensorMap q, k, v;                       // a sequence's step of Q rows, the caches' tiles
+  CUtensorMap all_q, prefix_k, prefix_v;     // PREFIX: all tokens' rows, the prefix's tiles
+};
+
+template <int D, int NT, int WR, bool PREFIX>
+__global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(const __grid_constant__ CacheMaps maps,
+                                                                                const CacheParams p) {
   using C = Cfg<D, NT, WR>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t s_base = smem_u32(smem);
@@ -267,7 +282,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
     mbar_fence_init();
   }
   launch_dependents();                            // the prefix parts may start beside this kernel
-  Walk walk(p, worker);
+  Walk<PREFIX> walk(p, worker);
   __syncthreads();
 
   if (warp == C::WARPS) {
@@ -275,16 +290,17 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
     uint32_t u = 0;                               // ring position: K of tile T at 2T, V at 2T + 1
     uint32_t seg = 0, loaded_q = 0;
     bool ok = true;
-    if (lane == 0 && walk.left > 0) { tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v); }
+    if (lane == 0 && walk.left > 0) { tma_prefetch_desc(&maps.q); tma_prefetch_desc(&maps.k); tma_prefetch_desc(&maps.v); }
     for (; ok && walk.left > 0; walk.next(), ++seg) {
       if (lane == 0) {
         const int qs = int(seg % C::QS);
         ok = seg < C::QS || mbar_wait_sleep(bar_q_empty(qs), ((seg / C::QS) - 1) & 1, abort_flag);
         if (ok) {
-          mbar_arrive_expect_tx(bar_q_full(qs), uint32_t(p.rows * D * 2));
+          const bool shared = walk.in_prefix();
+          mbar_arrive_expect_tx(bar_q_full(qs), uint32_t((shared ? p.prefix_rows : p.rows) * D * 2));
           for (int c = 0; c < D / 64; ++c)
-            tma_load_3d(s_base + C::OFF_Q + qs * C::Q_SLOT + c * C::QROWS * 128, &tm_q, c * 64, walk.kvh * p.group,
-                        walk.b * p.steps, bar_q_full(qs));
+            tma_load_3d(s_base + C::OFF_Q + qs * C::Q_SLOT + c * C::QROWS * 128, shared ? &maps.all_q : &maps.q, c * 64,
+                        walk.kvh * p.group, shared ? 0 : walk.b * p.steps, bar_q_full(qs));
           ++loaded_q;
         }
         const int64_t plane_row = (int64_t(walk.b) * p.kv_heads + walk.kvh) * p.capacity;
@@ -299,9 +315,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
               break;
             }
             mbar_arrive_expect_tx(bar_full(s), C::SLOT);
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_2d(s_base + C::OFF_KV + s * C::SLOT + c * kTile * 128, kv == 0 ? &tm_k : &tm_v, c * 64, row,
-                          bar_full(s));
+            for (int c = 0; c < D / 64; ++c) {
+              const uint32_t dst = s_base + C::OFF_KV + s * C::SLOT + c * kTile * 128;
+              if (walk.in_prefix())
+                tma_load_3d(dst, kv == 0 ? &maps.prefix_k : &maps.prefix_v, c * 64, walk.kvh, (walk.t0 + t) * kTile, bar_full(s));
+              else
+                tma_load_2d(dst, kv == 0 ? &maps.k : &maps.v, c * 64, row, bar_full(s));
+            }
           }
         }
         if (!ok) {
@@ -367,7 +387,10 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
       float of[D / 16][NT][4];                     // O^T: dims x rows
       float m[NT][2], l[NT][2];
       int lim[NT][2];                              // keys each row sees
-      const int base = walk.n - p.steps + 1;
+      // every row sees the whole prefix, a cache's row as far as its token
+      const bool shared = walk.in_prefix();
+      const int rows = shared ? p.prefix_rows : p.rows;
+      const int base = shared ? walk.n : walk.n - p.steps + 1;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -376,7 +399,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
         for (int e = 0; e < 2; ++e) {
           m[nt][e] = -INFINITY;
           l[nt][e] = 0.f;
-          lim[nt][e] = row_of(nt, e) < p.rows ? base + row_of(nt, e) / p.group : 0;
+          lim[nt][e] = row_of(nt, e) < rows ? base + (shared ? 0 : row_of(nt, e) / p.group) : 0;
         }
       }
       const int64_t plane = int64_t(walk.b) * p.kv_heads + walk.kvh;
@@ -430,7 +453,7 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
                 for (int e = 0; e < 4; ++e) {
                   float x = sf[i][nt][e] * c;
                   const int key = key0 + i * 16 + g + (e >> 1) * 8;
-                  if (p.scores != nullptr && row_of(nt, e & 1) < p.rows)
+                  if (p.scores != nullptr && !shared && row_of(nt, e & 1) < p.rows)
                     p.scores[(plane * p.rows + row_of(nt, e & 1)) * p.score_stride + key] = x;
                   if (masked && key >= lim[nt][e & 1]) x = -INFINITY;
                   sf[i][nt][e] = x;
@@ -551,7 +574,9 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
       }
       ok = group_sync();
       if (!ok) break;
-      const int64_t at = (plane + worker) * p.rows;
+      const int64_t at = shared ? int64_t(walk.kvh + worker) * rows : (plane + worker) * rows;
+      float* out_o = shared ? p.part_o : p.own_o;
+      float* out_lse = shared ? p.part_lse : p.own_lse;
 #pragma unroll 1
       for (int piece = part; piece < NT * (D / 16); piece += C::PARTS) {
         const int nt = piece / (D / 16), x = piece - nt * (D / 16);
@@ -578,13 +603,13 @@ __global__ void __launch_bounds__(Cfg<D, NT, WR>::THREADS, 1) cache_attn_kernel(
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int row = row_of(nt, e);
-          if (row < p.rows) {
+          if (row < rows) {
             const bool none = sum[e] == 0.f;       // a NaN sum goes through as NaN
             const float inv = none ? 0.f : __fdividef(1.f, sum[e]);
-            float* dst = p.own_o + (at + row) * D + x * 16 + g;
+            float* dst = out_o + (at + row) * D + x * 16 + g;
             dst[0] = none ? 0.f : acc[e] * inv;
             dst[8] = none ? 0.f : acc[e + 2] * inv;
-            if (x == 0 && g == 0) p.own_lse[at + row] = none ? -INFINITY : top[e] + __log2f(sum[e]);
+            if (x == 0 && g == 0) out_lse[at + row] = none ? -INFINITY : top[e] + __log2f(sum[e]);
           }
         }
       }
@@ -611,6 +636,7 @@ struct JoinParams {
   __nv_bfloat16* o;
   int64_t o_token, o_head;
   float* lse;
+  int prefix_len;                     // in the caches' list: its keys, else 0
   int row_blocks, chunks;             // blocks of joined rows; weight chunks per plane
 };
 
@@ -629,13 +655,28 @@ struct Parts {
   }
 };
 
-__device__ __forceinline__ Parts parts_of(const JoinParams& p, int b, int kvh, int r, int n, const Runs& runs, int before) {
+// The list's length, and the cost of the sequences before b (whole warp).
+__device__ __forceinline__ int list_length(const JoinParams& p, int b, int* before) {
+  const int shared = p.prefix_len > 0 ? plane_cost(tiles_of(p.prefix_len)) : 0;
+  return (count_cost(p.lens, p.B, p.capacity, b, before) + shared) * p.kv_heads;
+}
+
+__device__ __forceinline__ Parts parts_of(const JoinParams& p, int b, int kvh, int r, int n, int total, int before) {
+  const Runs runs(total, p.workers);
   Parts x;
   const int t = r / p.group, g = r - t * p.group;
+  const int64_t all = int64_t(p.B) * p.steps * p.group, row = (int64_t(b) * p.steps + t) * p.group + g;
   x.splits = p.splits;
-  x.prefix0 = (int64_t(kvh) * p.B * p.steps + int64_t(b) * p.steps + t) * p.group + g;
-  x.prefix_step = int64_t(p.kv_heads) * p.B * p.steps * p.group;
-  x.count = p.splits;
+  x.prefix0 = kvh * all + row;
+  x.prefix_step = p.kv_heads * all;
+  if (p.prefix_len > 0) {
+    const int tiles = tiles_of(p.prefix_len), s0 = total - (p.kv_heads - kvh) * plane_cost(tiles);
+    const int w0 = runs.worker(s0);
+    x.splits = runs.worker(s0 + tiles - 1) - w0 + 1;
+    x.prefix0 = (kvh + w0) * all + row;
+    x.prefix_step = all;
+  }
+  x.count = x.splits;
   x.own0 = 0;
   const int tiles = tiles_of(n);
   if (tiles > 0) {
@@ -688,9 +729,9 @@ __global__ void __launch_bounds__(kJoinThreads, SMALL ? 8 : 4) join_kernel(const
     int before = 0, total = 0, n = 0;
     if (p.workers > 0) {
       n = live_len(p.lens, b, p.capacity);
-      total = count_cost(p.lens, p.B, p.capacity, b, &before) * p.kv_heads;
+      total = list_length(p, b, &before);
     }
-    const Parts x = parts_of(p, b, kvh, r, n, Runs(total, p.workers), before);
+    const Parts x = parts_of(p, b, kvh, r, n, total, before);
     const int t = r / p.group, head = kvh * p.group + (r - t * p.group);
     wait_prerequisites();                          // the caller's lengths needed no wait
     constexpr int V = D / 32, AHEAD = SMALL ? 4 : 16;
@@ -758,8 +799,7 @@ __global__ void __launch_bounds__(kJoinThreads, SMALL ? 8 : 4) join_kernel(const
   const int n = live_len(p.lens, b, p.capacity);
   if (chunk * kChunk >= n) return;
   int before = 0;
-  const int total = count_cost(p.lens, p.B, p.capacity, b, &before) * p.kv_heads;
-  const Runs runs(total, p.workers);
+  const int total = list_length(p, b, &before);
   wait_prerequisites();
   // The weights so far and the first rows' scores are on their way while the rows' LSE is joined.
   constexpr int AHEAD = 4;
@@ -780,7 +820,7 @@ __global__ void __launch_bounds__(kJoinThreads, SMALL ? 8 : 4) join_kernel(const
   // Four rows a warp, eight lanes over each row's parts (all rows of a plane have as many).
   for (int r0 = warp * 4; r0 < p.rows; r0 += kJoinThreads / 8) {
     const int r = r0 + lane / 8, l8 = lane % 8;
-    const Parts x = parts_of(p, b, kvh, r < p.rows ? r : 0, n, runs, before);
+    const Parts x = parts_of(p, b, kvh, r < p.rows ? r : 0, n, total, before);
     const float mine = l8 < x.count ? x.lse(p, l8) : -INFINITY;
     float top = mine;
     for (int j = l8 + 8; j < x.count; j += 8) top = fmaxf(top, x.lse(p, j));
@@ -819,42 +859,46 @@ __global__ void __launch_bounds__(kJoinThreads, SMALL ? 8 : 4) join_kernel(const
     if (key + e < n) w[e] = old[e] + sum[e];
 }
 
-template <int D, int NT, int WR>
+template <int D, int NT, int WR, bool PREFIX>
 cudaError_t launch_cfg(const CacheAttnArgs& a, cudaStream_t stream, const char** why) {
   using C = Cfg<D, NT, WR>;
-  const int group = a.q_heads / a.kv_heads;
+  const int group = a.q_heads / a.kv_heads, tokens = a.B * a.steps;
   const int64_t rows = int64_t(a.B) * a.kv_heads * a.capacity;
-  CUtensorMap tq, tk, tv;
-  if (!make_heads_map(&tq, a.q, int64_t(a.B) * a.steps, a.q_heads, D, a.q_token, a.q_head, group, a.steps) ||
-      !make_rows_map(&tk, a.k_cache, rows, D, kTile) || !make_rows_map(&tv, a.v_cache, rows, D, kTile)) {
+  CacheMaps m = {};
+  if (!make_heads_map(&m.q, a.q, tokens, a.q_heads, D, a.q_token, a.q_head, group, a.steps) ||
+      !make_rows_map(&m.k, a.k_cache, rows, D, kTile) || !make_rows_map(&m.v, a.v_cache, rows, D, kTile) ||
+      (PREFIX && (!make_heads_map(&m.all_q, a.q, tokens, a.q_heads, D, a.q_token, a.q_head, group, tokens) ||
+                  !make_heads_map(&m.prefix_k, a.prefix_k, a.prefix_len, a.kv_heads, D, a.k_token, a.k_head, 1, kTile) ||
+                  !make_heads_map(&m.prefix_v, a.prefix_v, a.prefix_len, a.kv_heads, D, a.v_token, a.v_head, 1, kTile)))) {
     *why = "cuTensorMapEncodeTiled failed or is unavailable";
     return cudaErrorInvalidValue;
   }
   static DeviceFlags attr_set = {};
   const cudaError_t e = once_per_device(attr_set, [] {
-    return cudaFuncSetAttribute(cache_attn_kernel<D, NT, WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    return cudaFuncSetAttribute(cache_attn_kernel<D, NT, WR, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   });
   if (e != cudaSuccess) { *why = "cudaFuncSetAttribute(max dynamic smem) failed"; return e; }
   const CacheParams p{a.B, a.steps, a.kv_heads, group, a.steps * group, a.capacity, a.lens,
-                      a.scale * 1.4426950408889634f, a.own_o, a.own_lse, a.scores, a.score_stride, a.workers, a.err};
-  cache_attn_kernel<D, NT, WR><<<a.workers, C::THREADS, C::SMEM_BYTES, stream>>>(tq, tk, tv, p);
+                      a.scale * 1.4426950408889634f, a.own_o, a.own_lse, a.scores, a.score_stride, a.workers,
+                      PREFIX ? int(a.prefix_len) : 0, PREFIX ? tokens * group : 0, a.part_o, a.part_lse, a.err};
+  cache_attn_kernel<D, NT, WR, PREFIX><<<a.workers, C::THREADS, C::SMEM_BYTES, stream>>>(m, p);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool PREFIX>
 cudaError_t launch_rows(const CacheAttnArgs& a, cudaStream_t stream, const char** why) {
-  const int rows = a.steps * (a.q_heads / a.kv_heads);
-  if (rows <= 8) return launch_cfg<D, 1, 1>(a, stream, why);
-  if (rows <= 16) return launch_cfg<D, 2, 1>(a, stream, why);
-  if (rows <= 32) return launch_cfg<D, 2, 2>(a, stream, why);
-  return launch_cfg<D, 2, 4>(a, stream, why);
+  const int rows = (PREFIX ? a.B : 1) * a.steps * (a.q_heads / a.kv_heads);
+  if (rows <= 8) return launch_cfg<D, 1, 1, PREFIX>(a, stream, why);
+  if (rows <= 16) return launch_cfg<D, 2, 1, PREFIX>(a, stream, why);
+  if (PREFIX || rows <= 32) return launch_cfg<D, 2, 2, PREFIX>(a, stream, why);   // PREFIX: at most kListMaxRows
+  return launch_cfg<D, 2, 4, false>(a, stream, why);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, cudaStream_t stream, const char** why) {
-  if (a.d == 128) return launch_rows<128>(a, stream, why);
-  if (a.d == 64) return launch_rows<64>(a, stream, why);
+  if (a.d == 128) return a.with_prefix ? launch_rows<128, true>(a, stream, why) : launch_rows<128, false>(a, stream, why);
+  if (a.d == 64) return a.with_prefix ? launch_rows<64, true>(a, stream, why) : launch_rows<64, false>(a, stream, why);
   *why = "unsupported d";
   return cudaErrorInvalidValue;
 }
@@ -863,7 +907,7 @@ cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream) {
   const int group = a.q_heads / a.kv_heads, rows = a.steps * group;
   JoinParams p{a.B, a.steps, a.q_heads, a.kv_heads, group, rows, a.splits, a.capacity > 0 ? a.workers : 0, a.capacity, a.lens,
                a.part_o, a.part_lse, a.own_o, a.own_lse, a.scores, a.score_stride, a.weight,
-               static_cast<__nv_bfloat16*>(a.o), a.o_token, a.o_head, a.lse, 0, 0};
+               static_cast<__nv_bfloat16*>(a.o), a.o_token, a.o_head, a.lse, a.with_prefix ? int(a.prefix_len) : 0, 0, 0};
   const int64_t planes = int64_t(a.B) * a.kv_heads;
   p.row_blocks = int((planes * rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
   p.chunks = a.weight != nullptr ? int((a.capacity + kChunk - 1) / kChunk) : 0;

@@ -223,6 +223,8 @@ cudaError_t launch_packed(const PackedArgs& a, cudaStream_t stream, const char**
 // (cache_attn.cu).
 struct CacheAttnArgs {
   const void* q;
+  const void* prefix_k;
+  const void* prefix_v;
   const void* k_cache;
   const void* v_cache;
   const int32_t* lens;
@@ -231,11 +233,12 @@ struct CacheAttnArgs {
   float* weight;             // NULL or [B, kv_heads, capacity], added to
   int B, steps, q_heads, kv_heads, d;
   int64_t prefix_len, capacity;
-  int64_t q_token, q_head, o_token, o_head;
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head, o_token, o_head;   // k, v: the prefix's
   float scale;
-  int splits;                // prefix parts
-  const float* part_o;       // [splits, kv_heads, B * steps, group, d]
-  const float* part_lse;
+  int splits;                // prefix parts of the packed kernel
+  int with_prefix;           // 1: the prefix is a sequence of the cache pass (splits = 0)
+  float* part_o;             // [splits, kv_heads, B * steps, group, d], or with_prefix
+  float* part_lse;           //   [kv_heads + workers, B * steps, group, d]
   float* own_o;              // [slots, group * steps, d]
   float* own_lse;            // [slots, group * steps], log2 units
   float* scores;             // NULL or [B, kv_heads, group * steps, score_stride]
@@ -245,6 +248,8 @@ struct CacheAttnArgs {
 };
 // Most rows (query heads per key/value head x tokens per step) of one sequence.
 constexpr int kCacheMaxRows = 64;
+// Most rows of a whole batch whose prefix may be in the cache pass.
+constexpr int kListMaxRows = 32;
 // Most workers (CTAs) of the cache pass; it leaves at most one segment per (sequence, head) and
 // one per worker.
 constexpr int kCacheWorkers = 148;

@@ -101,6 +101,12 @@ SHAPES = {
     "rows_64": (2, 64, 2, 2, 64, 70, 190, [190, 63]),
     "long_prefix": (5, 1, 10, 2, 128, 5000, 70, [1, 2, 3, 70, 9]),
     "long_cache": (2, 1, 4, 1, 128, 3, 30000, [29999, 17]),
+    # batches of at most 32 rows: the prefix in the caches' list
+    "list_rows_20": (2, 5, 16, 8, 64, 1097, 518, [219, 500]),
+    "list_one_head": (3, 2, 1, 1, 128, 500, 700, [2, 700, 65]),
+    "list_empty_caches": (2, 1, 4, 4, 64, 300, 50, [0, 0]),
+    "list_rows_32": (4, 1, 32, 4, 128, 90, 130, [64, 0, 129, 130]),
+    "list_many_heads": (1, 4, 16, 16, 128, 65, 64, [4]),
     "many_planes": (83, 1, 60, 12, 64, 462, 24, [(5 * i) % 25 for i in range(83)]),
     "many_sequences": (150, 1, 2, 1, 64, 20, 80, [(7 * i) % 81 for i in range(150)]),
 }
