@@ -525,16 +525,16 @@ lva_status lva_packed_attn(const lva_packed_params* p, const void* q, const void
 // 128 keys, 0.9 us).  `join` is what a part's rows cost the join, written and read (about
 // 7.2 MB a block time).  The caches, taken as half full (the lengths are on the device), cost
 // their bytes at 5.9 MB a block time, or a worker its share of the tiles, 0.5 (8 rows) to 1.9
-// (64 rows) each and 0.6 of that with d = 64, and of the planes' starts and ends, 2.5 (4 rows)
-// to 5.5 (16 rows) each, as fitted to 52 to 148 workers alone.
+// (64 rows) each and 0.6 of that with d = 64, and of the planes' starts and ends, 1.5 to 2.5 (4
+// rows) to 5.5 (16 rows) each, as fitted to 52 to 148 workers alone.
 //   In turn: 148 workers, then the parts.  With c = items * parts CTAs the parts take about
 //   blocks / parts when c <= 148, or items * blocks / 148 and half a part of tail when there
 //   are more, and in either case 3 for a part's start and end; 13 for the launches and the
 //   join, up to 8 more when the caches keep the SMs from the parts.
 //   In one list: where all tokens of the batch are at most 32 rows, the prefix can be one more
-//   sequence of the cache pass, at the tiles' cost for that many rows; 12 for two launches
-//   instead of three, 0.12 for each piece that the join finds of a row.  The other forms are
-//   kept unless this one is clearly shorter (the lengths may be above the estimate).
+//   sequence of the cache pass, at the tiles' cost for that many rows, 0.12 for each piece that
+//   the join finds of a row, and 12 for two launches instead of three.  It is taken where it is
+//   clearly shorter: at 15 and 1.8 times its work.
 //   Beside one another: a part's CTA and a worker have an SM each, parts and workers 148 together
 //   and at least 52 workers.
 // 8,192 prefix keys and 32 caches of up to 1,024 (8 heads of 128, 32 query heads): 35.8 us in
@@ -545,6 +545,12 @@ lva_status lva_packed_attn(const lva_packed_params* p, const void* q, const void
 static double tile_cost(int rows, int d) {
   const int padded = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   return (0.35 + 0.024 * padded) * (d == 64 ? 0.6 : 1.0);
+}
+
+// A plane's tiles, its start and its end; the start hides behind the tiles when there are several.
+static double plane_work(double tiles, double tile, double rows) {
+  const double many = tiles * tile + 0.5, few = tile + 1.5;
+  return (many > few ? many : few) + 0.25 * rows;
 }
 
 static void prefix_split(const lva_shared_prefix_params* p, int* parts, int* workers, int* with_prefix) {
@@ -558,7 +564,7 @@ static void prefix_split(const lva_shared_prefix_params* p, int* parts, int* wor
   const double join = double(p->B) * p->steps * p->q_heads * (p->d * 8 + 8) / 7.2e6;
   const double planes = p->capacity > 0 ? double(p->B) * p->kv_heads : 0;
   const double bytes = planes * p->capacity * p->d * 2 / 5.9e6;
-  const double work = planes * (double(p->capacity / 128 + 1) * tile_cost(rows, p->d) + 1.5 + 0.25 * rows);
+  const double work = planes * plane_work(double(p->capacity / 128 + 1), tile_cost(rows, p->d), rows);
   auto caches = [&](double n) { return bytes > work / n ? bytes : work / n; };
   const double all = caches(kCacheWorkers), kept = 2 * all < 8 ? 2 * all : 8;
   double best = 0;
@@ -576,9 +582,9 @@ static void prefix_split(const lva_shared_prefix_params* p, int* parts, int* wor
   if (p->capacity == 0 || all_rows > kListMaxRows || list >= double(int64_t(1) << 31)) return;
   const double wide = tile_cost(int(all_rows), p->d), places = planes * double(p->capacity / 128 + 6) + p->kv_heads * (tiles + 5);
   const double pieces = places > kCacheWorkers ? (tiles + 5) * kCacheWorkers / places : tiles;
-  const double one = (planes * (double(p->capacity / 128 + 1) * wide + 1.5 + 0.25 * rows) +
-                      p->kv_heads * (tiles * wide + 1.5 + 0.25 * all_rows)) / kCacheWorkers + 0.12 * pieces + 12;
-  if (1.4 * one < best) { *parts = 0; *workers = kCacheWorkers; *with_prefix = 1; }
+  const double one = (planes * plane_work(double(p->capacity / 128 + 1), wide, rows) +
+                      p->kv_heads * plane_work(tiles, wide, all_rows)) / kCacheWorkers + 0.12 * pieces;
+  if (15 + 1.8 * one < best) { *parts = 0; *workers = kCacheWorkers; *with_prefix = 1; }
 }
 
 // Byte offsets of the workspace's pieces (256-byte steps).
