@@ -93,3 +93,28 @@ def test_runs_cover_every_tile_once_and_the_join_finds_them(seed):
             plane = b * heads + h
             assert [plane + w for w in range(w0, w1 + 1)] == sorted(s for s, q in slots.items() if q == plane)
         before += cost(t)
+
+
+@pytest.mark.parametrize("seed", range(100))
+def test_a_prefix_as_the_last_sequence_has_slots_of_its_own(seed):
+    # its segments are numbered head + worker in a buffer of their own, which holds
+    # heads + workers of them, and the join finds them from the list's end
+    rng = random.Random(1000 + seed)
+    heads, workers = rng.choice([1, 2, 3, 8, 12]), 148
+    lens = [rng.choice([0, 1, 64, 65, rng.randint(0, 3000)]) for _ in range(rng.randint(1, 32))]
+    prefix = rng.choice([1, 64, 65, rng.randint(1, 500), rng.randint(1, 9000)])
+    total = (sum(cost(tiles_of(n)) for n in lens) + cost(tiles_of(prefix))) * heads
+    runs, slots = Runs(total, workers), {}
+    for w in range(workers):
+        for plane, t0, count in walk(lens + [prefix], heads, runs, w):
+            kvh = plane - len(lens) * heads
+            if kvh >= 0:
+                assert kvh + w not in slots and kvh + w < heads + workers
+                slots[kvh + w] = kvh
+            else:
+                assert plane + w < len(lens) * heads + workers       # the caches' slots stay inside theirs
+    t = tiles_of(prefix)
+    for h in range(heads):
+        s0 = total - (heads - h) * cost(t)
+        w0, w1 = runs.worker(s0), runs.worker(s0 + t - 1)
+        assert [h + w for w in range(w0, w1 + 1)] == sorted(s for s, q in slots.items() if q == h)
