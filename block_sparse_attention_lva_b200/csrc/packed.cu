@@ -740,7 +740,8 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
 
     // A block that every row sees, after the first: exponentials against the current
     // reference while the block max is found alongside; given up (2) before anything is
-    // stored when a row's max outgrows its reference by 2^8.
+    // stored when a row's max outgrows its reference by 2^8, or is NaN: the polynomial's clamp
+    // drops a NaN, step() lets it through.
     auto step_spec = [&]() -> int {
       const int b = int(T % C::NSB);
       if (!__all_sync(0xffffffffu, mbar_wait(bar_s_full(b), int(T / C::NSB) & 1, abort_flag))) return 0;
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
       uint32_t pk[HALF / 2];
 #pragma unroll
       for (int e = 0; e < HALF / 2; ++e) {
-        m4[e & 3] = fmax3(m4[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+        m4[e & 3] = fmax3_nan(m4[e & 3], __uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
         const uint64_t x2 = f2_fma(f2_pack_bits(sr[2 * e], sr[2 * e + 1]), c2, nm2);
         uint64_t p2;
         if (poly_pair(e)) {
@@ -772,9 +773,10 @@ __global__ void __launch_bounds__(kThreads, 1) packed_attn_kernel(
         f2_unpack(p2, p0, p1);
         pk[e] = pack_bf16x2(p0, p1);
       }
-      float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      if (__any_sync(0xffffffffu, sees && (mx > m_ref + kRescaleThreshold || m_ref == -INFINITY))) return 2;
+      float mx = fmax3_nan(fmax3_nan(m4[0], m4[1], m4[2]), m4[3], m4[3]) * c;
+      const float far = __shfl_xor_sync(0xffffffffu, mx, 16);
+      mx = fmax3_nan(mx, far, far);
+      if (__any_sync(0xffffffffu, sees && (!(mx <= m_ref + kRescaleThreshold) || m_ref == -INFINITY))) return 2;
       tmem_st_16x2_32<HALF / 2>(tmem + lane_off + C::TM_S + 128 * b, *reinterpret_cast<const uint32_t(*)[32]>(pk));
       tmem_wait_st();
       float a0, a1, b0, b1;
