@@ -14,7 +14,7 @@ from ._binding import (LVA_MASK_ALL, LVA_MASK_LVSA_FRAMES, LVA_MASK_STATIC, LVA_
                        lva_build_block_mask_noalloc,
                        lva_device_error, lva_reorder_tokens, lva_select_blocks,
                        lva_selftest_wait, lva_version, lva_layer_step_host, lva_packed_attn, lva_packed_workspace_bytes, lva_append_cache,
-                       lva_evict_cache, lva_shared_prefix_attn, lva_shared_prefix_workspace_bytes)
+                       lva_evict_cache, lva_shared_prefix_attn, lva_shared_prefix_plan, lva_shared_prefix_workspace_bytes)
 from .pipeline import SquadTwoPass, StaticMaskCalibrator, VideoBlockSparseAttention, mask_params_for
 from .sharding import HeadShard, head_range, shard_rows
 
@@ -25,6 +25,6 @@ __all__ = ["LVA_MASK_ALL", "LVA_MASK_LVSA_FRAMES", "LVA_MASK_STATIC", "LVA_MASK_
            "lva_device_error", "lva_reorder_tokens", "lva_version",
            "lva_block_energy", "lva_select_blocks", "lva_aggregate_masks", "lva_block_sparse_attn_raster", "lva_block_sparse_lse",
            "lva_window_transposed_attn", "lva_selftest_wait", "lva_layer_step_host", "lva_packed_attn", "lva_packed_workspace_bytes", "lva_append_cache", "lva_evict_cache",
-           "lva_shared_prefix_attn", "lva_shared_prefix_workspace_bytes",
+           "lva_shared_prefix_attn", "lva_shared_prefix_plan", "lva_shared_prefix_workspace_bytes",
            "SquadTwoPass", "StaticMaskCalibrator", "VideoBlockSparseAttention", "mask_params_for",
            "HeadShard", "head_range", "shard_rows"]

@@ -95,6 +95,7 @@ SIGNATURES = {
     "lva_packed_workspace_bytes": (_c_i64, [_params]),
     "lva_packed_attn": (_c_int, [_params, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _vp]),
     "lva_shared_prefix_workspace_bytes": (_c_i64, [_params, _c_int]),
+    "lva_shared_prefix_plan": (_c_int, [_params, ctypes.POINTER(_c_int), ctypes.POINTER(_c_int), ctypes.POINTER(_c_int)]),
     "lva_shared_prefix_attn": (_c_int, [_params, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                         _vp, _vp, _c_i64, _vp]),
     "lva_append_cache": (_c_int, [_vp, _vp, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int,
@@ -578,6 +579,16 @@ def lva_shared_prefix_workspace_bytes(B: int, steps: int, q_heads: int, kv_heads
     """Workspace bytes of ``lva_shared_prefix_attn`` for these sizes (-1 for sizes it refuses)."""
     p = _PREFIX.pack(B, steps, q_heads, kv_heads, d, 1.0, prefix_len, capacity, *[0] * 8)
     return lib.lva_shared_prefix_workspace_bytes(p, 1 if with_weight else 0)
+
+
+def lva_shared_prefix_plan(B: int, steps: int, q_heads: int, kv_heads: int, d: int, prefix_len: int, capacity: int):
+    """(parts of the prefix, workers of the cache pass, whether the prefix is one more sequence of that pass) of
+    ``lva_shared_prefix_attn`` for these sizes."""
+    out = [_c_int() for _ in range(3)]
+    p = _PREFIX.pack(B, steps, q_heads, kv_heads, d, 1.0, prefix_len, capacity, *[0] * 8)
+    _check(lib.lva_shared_prefix_plan(p, *[ctypes.byref(x) for x in out]))
+    parts, workers, in_list = [x.value for x in out]
+    return parts, workers, bool(in_list)
 
 
 def lva_shared_prefix_attn(q, prefix_k, prefix_v, k_cache, v_cache, lens, o, lse, workspace, scale: float, weight=None):

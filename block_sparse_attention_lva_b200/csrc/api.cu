@@ -630,6 +630,17 @@ int64_t lva_shared_prefix_workspace_bytes(const lva_shared_prefix_params* p, int
   return prefix_plan(p, with_weight != 0, &w) == LVA_OK ? w.bytes : -1;
 }
 
+lva_status lva_shared_prefix_plan(const lva_shared_prefix_params* p, int* parts, int* workers, int* in_list) {
+  PrefixWorkspace w;
+  const lva_status s = prefix_plan(p, false, &w);
+  if (s != LVA_OK) return s;
+  if (!parts || !workers || !in_list) return fail(LVA_ERR_INVALID_ARG, "shared_prefix_plan: null pointer");
+  *parts = w.parts;
+  *workers = w.workers;
+  *in_list = w.with_prefix;
+  return ok();
+}
+
 lva_status lva_shared_prefix_attn(const lva_shared_prefix_params* p, const void* q, const void* prefix_k,
                                   const void* prefix_v, const void* k_cache, const void* v_cache,
                                   const int32_t* lens, void* o, float* lse, float* weight, void* workspace,

@@ -586,6 +586,17 @@ lva_status lva_shared_prefix_attn(const lva_shared_prefix_params* params, const 
                                   cudaStream_t stream);
 
 /*
+ * lva_shared_prefix_plan -- how lva_shared_prefix_attn cuts a call of these sizes: a diagnostic
+ * (the results are the same to rounding however it is cut).
+ *
+ * parts: parts that the prefix is cut into along its keys (0: it is not cut apart), in_list: 1
+ * when it is one more sequence of the cache pass instead; workers: thread blocks of the cache
+ * pass, 148 unless parts run beside them on multiprocessors of their own.  Host only: nothing is
+ * launched.  Errors: those of the sizes, and LVA_ERR_INVALID_ARG for null pointers.
+ */
+lva_status lva_shared_prefix_plan(const lva_shared_prefix_params* params, int* parts, int* workers, int* in_list);
+
+/*
  * lva_append_cache -- put a step's tokens into the caches.
  *
  * Row lens[b] + t of every head of sequence b's caches takes token t of k_new, v_new, its
