@@ -39,7 +39,10 @@
 //                      request, weight[c] += sum_r 2^(x_rc - LSE_r) from the scores the first
 //                      kernel left (4 R bytes per key against 2 d for reading K again).
 //                      Each weight has one writer and a fixed order of additions.
+//                      A row of several tokens' step that came out not finite is looked at again
+//                      (without_late_keys).
 #include <cstdint>
+#include <type_traits>
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -638,6 +641,12 @@ struct JoinParams {
   float* lse;
   int prefix_len;                     // in the caches' list: its keys, else 0
   int row_blocks, chunks;             // blocks of joined rows; weight chunks per plane
+  // for rows that are summed up again (without_late_keys)
+  const __nv_bfloat16* q;
+  int64_t q_token, q_head;
+  const __nv_bfloat16* k_cache;
+  const __nv_bfloat16* v_cache;
+  float scale_log2;
 };
 
 constexpr int kJoinThreads = 128;
@@ -712,12 +721,85 @@ __device__ __forceinline__ float join_lse(const JoinParams& p, const Parts& x, f
   return sum == 0.f ? -INFINITY : use + __log2f(sum);
 }
 
+// A lane's share of a row.
+template <int V>
+struct Share { float v[V]; };
+
+template <int V>
+__device__ __forceinline__ Share<V> load_bf16(const __nv_bfloat16* src) {
+  Share<V> x;
+#pragma unroll
+  for (int e = 0; e < V; e += 2) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(src + e);
+    x.v[e] = __uint_as_float(w << 16);
+    x.v[e + 1] = __uint_as_float(w & 0xffff0000u);
+  }
+  return x;
+}
+__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+
+template <int V>
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* dst, const float (&v)[V]) {
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(v[0], v[1]);
+}
+
+// Stores a token's row that came out not finite.  The cache pass multiplies V of whole tiles, and
+// where V is not finite at a live key that only the step's later tokens see, zero, this row's
+// weight there, times it is NaN.  Such columns are summed up again, in float32: the prefix's
+// parts, and the cache keys that the row sees one by one.  Whole warp, a lane its D / 32 columns;
+// out of line and last, so that the other rows do not pay for it.
+template <int D>
+__device__ __noinline__ void without_late_keys(const JoinParams& p, int row, int n, int total, int before, float lse, Share<D / 32> acc) {
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31, plane = row / p.rows, r = row - plane * p.rows;
+  const int b = plane / p.kv_heads, kvh = plane - b * p.kv_heads, t = r / p.group, head = kvh * p.group + r - t * p.group;
+  const int seen = n - p.steps + 1 + t > 0 ? n - p.steps + 1 + t : 0;
+  const int64_t first = int64_t(plane) * p.capacity * D + lane * V, token = int64_t(b) * p.steps + t;
+  bool late[V] = {}, some = false;
+  for (int key = seen; key < n; ++key) {
+    const Share<V> v = load_bf16<V>(p.v_cache + first + int64_t(key) * D);
+#pragma unroll
+    for (int e = 0; e < V; ++e) late[e] |= not_finite(v.v[e]) && not_finite(acc.v[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) some |= late[e];
+  if (__any_sync(kFull, some)) {
+    const Parts x = parts_of(p, b, kvh, r, n, total, before);
+    float sum[V] = {};
+    for (int j = 0; j < x.splits; ++j) {
+      const float a = ex2_approx(x.lse(p, j) - lse);
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum[e] = fmaf(a, p.part_o[x.at(p, j) * D + lane * V + e], sum[e]);
+    }
+    const Share<V> q = load_bf16<V>(p.q + token * p.q_token + int64_t(head) * p.q_head + lane * V);
+    for (int key = 0; key < seen; ++key) {
+      const Share<V> k = load_bf16<V>(p.k_cache + first + int64_t(key) * D), v = load_bf16<V>(p.v_cache + first + int64_t(key) * D);
+      float dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) dot = fmaf(q.v[e], k.v[e], dot);
+      const float a = ex2_approx(warp_sum(dot) * p.scale_log2 - lse);
+      // (a weight is positive, if too small for a float)
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum[e] = not_finite(v.v[e]) ? sum[e] + v.v[e] : fmaf(a, v.v[e], sum[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (late[e]) acc.v[e] = sum[e];
+  }
+  store_bf16<V>(p.o + token * p.o_token + int64_t(head) * p.o_head + lane * V, acc.v);
+}
+
 // WEIGHTS: blocks for the weights follow those of the rows.  SMALL: fewer O parts in flight, so that
 // eight blocks fit an SM instead of four, for long lists of blocks over few parts (16 caches of
 // up to 6,000 keys, 12 heads, 4 tokens: the call takes 77 us, 80 in the other form; 2 tokens over
 // 5,448 shared keys in 22 parts take 23 us so, 21 in the other).
-template <int D, bool WEIGHTS, bool SMALL>
-__global__ void __launch_bounds__(kJoinThreads, SMALL ? 8 : 4) join_kernel(const JoinParams p) {
+// LATE: several tokens a step; a look at the sums, 0 to 0.5 us a call (16 caches of up to 6,000
+// keys, 12 heads, 4 tokens, with weights: 80.3 us, 79.9 without it).
+template <int D, bool WEIGHTS, bool SMALL, bool LATE>
+__global__ void __launch_bounds__(kJoinThreads, SMALL ? 8 : 4) join_kernel(const __grid_constant__ JoinParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (!WEIGHTS || int(blockIdx.x) < p.row_blocks) {
     // One warp per row: O and LSE.
@@ -782,12 +864,20 @@ __global__ void __launch_bounds__(kJoinThreads, SMALL ? 8 : 4) join_kernel(const
         for (int e = 0; e < V; ++e) acc[e] = fmaf(w, v[e], acc[e]);
       }
     }
-    __nv_bfloat16* dst = p.o + (int64_t(b) * p.steps + t) * p.o_token + int64_t(head) * p.o_head + lane * V;
-    if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
-    else
-      *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0], acc[1]);
     if (lane == 0) p.lse[(int64_t(b) * p.q_heads + head) * p.steps + t] = lse * kLn2;
+    if constexpr (LATE) {
+      bool odd = false;
+#pragma unroll
+      for (int e = 0; e < V; ++e) odd |= not_finite(acc[e]);
+      if (__any_sync(kFull, odd)) {
+        Share<V> all;
+#pragma unroll
+        for (int e = 0; e < V; ++e) all.v[e] = acc[e];
+        without_late_keys<D>(p, int(row), n, total, before, use, all);
+        return;
+      }
+    }
+    store_bf16<V>(p.o + (int64_t(b) * p.steps + t) * p.o_token + int64_t(head) * p.o_head + lane * V, acc);
     return;
   }
   // A chunk of one plane's keys: the weight they collected.
@@ -907,7 +997,9 @@ cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream) {
   const int group = a.q_heads / a.kv_heads, rows = a.steps * group;
   JoinParams p{a.B, a.steps, a.q_heads, a.kv_heads, group, rows, a.splits, a.capacity > 0 ? a.workers : 0, a.capacity, a.lens,
                a.part_o, a.part_lse, a.own_o, a.own_lse, a.scores, a.score_stride, a.weight,
-               static_cast<__nv_bfloat16*>(a.o), a.o_token, a.o_head, a.lse, a.with_prefix ? int(a.prefix_len) : 0, 0, 0};
+               static_cast<__nv_bfloat16*>(a.o), a.o_token, a.o_head, a.lse, a.with_prefix ? int(a.prefix_len) : 0, 0, 0,
+               static_cast<const __nv_bfloat16*>(a.q), a.q_token, a.q_head, static_cast<const __nv_bfloat16*>(a.k_cache),
+               static_cast<const __nv_bfloat16*>(a.v_cache), a.scale * 1.4426950408889634f};
   const int64_t planes = int64_t(a.B) * a.kv_heads;
   p.row_blocks = int((planes * rows + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
   p.chunks = a.weight != nullptr ? int((a.capacity + kChunk - 1) / kChunk) : 0;
@@ -915,9 +1007,13 @@ cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream) {
   // more blocks than the large form has room for at once, and parts within the small one's loads
   const bool small = p.chunks > 0 && blocks > 4u * unsigned(sm_count()) && a.splits <= 4;
   auto launch = [&](auto kernel) { return launch_dependent(kernel, blocks, kJoinThreads, 0, stream, p); };
-  if (small) return a.d == 128 ? launch(join_kernel<128, true, true>) : launch(join_kernel<64, true, true>);
-  if (p.chunks > 0) return a.d == 128 ? launch(join_kernel<128, true, false>) : launch(join_kernel<64, true, false>);
-  return a.d == 128 ? launch(join_kernel<128, false, false>) : launch(join_kernel<64, false, false>);
+  auto form = [&](auto late) {
+    constexpr bool LATE = decltype(late)::value;
+    if (small) return a.d == 128 ? launch(join_kernel<128, true, true, LATE>) : launch(join_kernel<64, true, true, LATE>);
+    if (p.chunks > 0) return a.d == 128 ? launch(join_kernel<128, true, false, LATE>) : launch(join_kernel<64, true, false, LATE>);
+    return a.d == 128 ? launch(join_kernel<128, false, false, LATE>) : launch(join_kernel<64, false, false, LATE>);
+  };
+  return a.steps > 1 && a.capacity > 0 ? form(std::true_type{}) : form(std::false_type{});
 }
 
 }  // namespace lva

@@ -546,7 +546,8 @@ lva_status lva_packed_attn(const lva_packed_params* params, const void* q, const
  * the cache keys c <= lens[b] - steps + t; with
  *   LSE = ln sum_c exp(scale <q, k_c>),  O = sum_c exp(scale <q, k_c> - LSE) v_c
  * over both.  lse: device, fp32 [B, q_heads, steps].  A token that sees no key gets O = 0 and
- * LSE = -inf.  Cache entries from lens[b] on never matter, whatever memory holds there.
+ * LSE = -inf.  Cache entries from lens[b] on never matter, whatever memory holds there,
+ * nor does an entry of a later token of the step to an earlier one (it does not see it).
  *
  * weight: NULL, or device, fp32 [B, kv_heads, capacity], to which every live cache key's
  * attention probabilities, summed over the step's tokens and the heads of its group, are
