@@ -535,7 +535,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def lva_packed_workspace_bytes(sequences: int, q_heads: int, kv_heads: int, d: int, total_q: int, total_k: int) -> int:
     """Workspace bytes of ``lva_packed_attn`` for these sizes (0: none needed; -1: refused)."""
-    return lib.lva_packed_workspace_bytes(_PACKED.pack(sequences, q_heads, kv_heads, d, 1, 1.0, total_q, total_k, *[0] * 8))
+    try:
+        p = _PACKED.pack(sequences, q_heads, kv_heads, d, 1, 1.0, total_q, total_k, *[0] * 8)
+    except struct.error:             # a size that its C type does not hold
+        return -1
+    return lib.lva_packed_workspace_bytes(p)
 
 
 _packed_size = functools.lru_cache(maxsize=1024)(lva_packed_workspace_bytes)    # by sizes alone
@@ -577,7 +581,10 @@ def lva_packed_attn(q, k, v, o, lse, cu_q, cu_k, scale: float, causal: bool = Tr
 def lva_shared_prefix_workspace_bytes(B: int, steps: int, q_heads: int, kv_heads: int, d: int, prefix_len: int,
                                       capacity: int, with_weight: bool = False) -> int:
     """Workspace bytes of ``lva_shared_prefix_attn`` for these sizes (-1 for sizes it refuses)."""
-    p = _PREFIX.pack(B, steps, q_heads, kv_heads, d, 1.0, prefix_len, capacity, *[0] * 8)
+    try:
+        p = _PREFIX.pack(B, steps, q_heads, kv_heads, d, 1.0, prefix_len, capacity, *[0] * 8)
+    except struct.error:             # a size that its C type does not hold
+        return -1
     return lib.lva_shared_prefix_workspace_bytes(p, 1 if with_weight else 0)
 
 
@@ -585,7 +592,10 @@ def lva_shared_prefix_plan(B: int, steps: int, q_heads: int, kv_heads: int, d: i
     """(parts of the prefix, workers of the cache pass, whether the prefix is one more sequence of that pass) of
     ``lva_shared_prefix_attn`` for these sizes."""
     out = [_c_int() for _ in range(3)]
-    p = _PREFIX.pack(B, steps, q_heads, kv_heads, d, 1.0, prefix_len, capacity, *[0] * 8)
+    try:
+        p = _PREFIX.pack(B, steps, q_heads, kv_heads, d, 1.0, prefix_len, capacity, *[0] * 8)
+    except struct.error as e:
+        _refuse(f"a size is out of range: {e}")
     _check(lib.lva_shared_prefix_plan(p, *[ctypes.byref(x) for x in out]))
     parts, workers, in_list = [x.value for x in out]
     return parts, workers, bool(in_list)
