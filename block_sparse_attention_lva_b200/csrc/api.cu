@@ -531,14 +531,16 @@ lva_status lva_packed_attn(const lva_packed_params* p, const void* q, const void
 //   blocks / parts when c <= 148, or items * blocks / 148 and half a part of tail when there
 //   are more, and in either case 3 for a part's start and end; 13 for the launches and the
 //   join, up to 8 more when the caches keep the SMs from the parts.
+//   (148, and 74 tiles for packed parts above, are a B200's SMs and half of them: what the
+//   estimates were fitted to.  Any count is right.)
 //   In one list: where all tokens of the batch are at most 32 rows, the prefix can be one more
 //   sequence of the cache pass, at the tiles' cost for that many rows, 0.12 for each piece that
 //   the join finds of a row, and 12 for two launches instead of three.  It is taken where it is
 //   clearly shorter: at 15 and 1.8 times its work.
 //   Beside one another: a part's CTA and a worker have an SM each, parts and workers 148 together
 //   and at least 52 workers.
-// 8,192 prefix keys and 32 caches of up to 1,024 (8 heads of 128, 32 query heads): 35.8 us in
-// turn, 29 to 31 beside with 4 to 6 parts; 30,000 keys, 40 query heads: 55.9 and 53; 65,531 keys
+// In loops over one state: 8,192 prefix keys and 32 caches of up to 1,024 (8 heads of 128, 32 query
+// heads): 35.8 us in turn, 29 to 31 beside with 4 to 6 parts (32 to 33 among other calls); 30,000 keys, 40 query heads: 55.9 and 53; 65,531 keys
 // and 96 caches of up to 4,096: 311 and 290; 462 keys, 83 tiny caches of 12 heads: 42 and 66.
 // 1,050 prefix keys, one cache, 4 rows: 16.3 us beside, 14.1 in one list; 9 keys, two caches, 2
 // rows: 16.4 and 14.0; with 44 to 64 rows 16 to 18 and 17 to 31.

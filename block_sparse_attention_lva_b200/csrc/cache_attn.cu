@@ -8,8 +8,10 @@
 //   x_rc = scale log2(e) <q_r, k_c>,  m = max_c x_rc,  l = sum_c 2^(x_rc - m),
 //   O_r = sum_c 2^(x_rc - m) v_c / l,  LSE_r = m + log2 l   (log2 units)
 //
-// The bound is the cache's bytes from HBM (4 d per key and plane; a row costs 4 d flops per
-// key, R <= 64 of them).  Work is cut without looking at single sequences: the 64-key tiles
+// With up to 8 rows the bound is the cache's bytes from HBM (4 d per key and plane; a row costs
+// 4 d flops per key, R <= 64 of them); with more it is the warps' products and softmax, and with
+// d = 128 these forms spill 136 to 240 bytes a thread: 16 caches of 3,000 to 6,000 keys, 8 heads of
+// 128 (295 MB, 45 us) take 53, 62, 81 and 125 us with 4, 16, 32 and 64 rows.  Work is cut without looking at single sequences: the 64-key tiles
 // of all planes form one list, and each worker (a CTA, one per SM) takes an equal run of it,
 // so ragged lengths balance by themselves.  A run may begin and end inside a plane; every
 // (plane, worker) segment leaves its normalised O and LSE in float32.  Segments of the list,

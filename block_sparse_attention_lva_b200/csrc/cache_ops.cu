@@ -539,8 +539,9 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   p.budget = a.budget;
   if (a.k_out == a.k_cache) {
     // Slices of at least 32 bytes (a DRAM sector) until there are three CTAs for an SM: 96
-    // planes of 8,192 kept rows 184 us with slices of 128 bytes, 154 with 64; 64 planes of
-    // 20,000 rows 272 with 64 bytes, 290 with 32; 32 planes of 8,192 rows 74 and 69.
+    // planes of 8,192 kept rows 268 us whole, 198 with slices of 128 bytes, 193 with 64, 195 with
+    // 32; 64 planes of 20,000 rows 643, 401, 293 and 339; 32 planes of 8,192 rows 222, 129, 83 and
+    // 79; 230 planes of 4,096 rows 217, 216, 210 and 229 (weights that are new in every call).
     p.slices = 1;
     while (p.slices < p.units / 2 && planes * 2 * p.slices < 3 * sm_count()) p.slices *= 2;
     move_in_place_kernel<<<unsigned(planes * (2 * p.slices + 1)), kMoveThreads, 0, stream>>>(p);
